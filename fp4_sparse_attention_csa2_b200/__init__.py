@@ -16,9 +16,9 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 # checks); it is never loaded otherwise
 LIB_PATH = os.path.join(HERE, "libcsa2_debug.so" if os.environ.get("CSA2_LIBRARY") == "debug" else "libcsa2.so")
 
-OK, ERR_INVALID_ARG, ERR_UNSUPPORTED, ERR_CUDA, ERR_TIMEOUT, ERR_DEVICE_BOUNDS = range(6)
+OK, ERR_INVALID_ARG, ERR_UNSUPPORTED, ERR_CUDA, ERR_TIMEOUT, ERR_DEVICE_BOUNDS, ERR_NONFINITE = range(7)
 FULL, REINDEX, REUSE = 0, 1, 2
-F32, BF16, E4M3 = 0, 1, 2
+F32, BF16, E4M3, F16 = 0, 1, 2, 3
 
 ABI_FUNCTIONS = (
     "csa2_workspace_bytes", "csa2_workspace_init", "csa2_kv_append_quant", "csa2_kv_export_rows",
@@ -29,6 +29,8 @@ ABI_FUNCTIONS = (
     "csa2_cp_index_local", "csa2_cp_reindex_local", "csa2_cp_reindex_select", "csa2_cp_merge_workspace_bytes",
     "csa2_cp_merge_select",
     "csa2_cp_sparse_swa_attn", "csa2_lse_merge",
+    "csa2_kv8_workspace_bytes", "csa2_kv8_append", "csa2_kv8_read", "csa2_kv8_attn", "csa2_kv8_select_blocks",
+    "csa2_kv8_block_attn",
     "csa2_read_device_status", "csa2_status_string", "csa2_debug_set_wait_limit", "csa2_debug_default_wait_limit",
     "csa2_debug_encode",
 )
@@ -47,6 +49,16 @@ class csa2_cache(ctypes.Structure):
         ("page_size", ctypes.c_int32), ("dim", ctypes.c_int32), ("idx_dim", ctypes.c_int32),
         ("row_stride", ctypes.c_int32), ("seq_stride_slots", ctypes.c_int64), ("n_slots", ctypes.c_int64),
         ("idx_key_dtype", ctypes.c_int),
+    ]
+
+
+class csa2_kv8_cache(ctypes.Structure):
+    _fields_ = [
+        ("k_codes", ctypes.c_void_p), ("v_codes", ctypes.c_void_p), ("k_scale", ctypes.c_void_p),
+        ("v_scale", ctypes.c_void_p), ("k_bounds", ctypes.c_void_p), ("block_table", ctypes.c_void_p),
+        ("seq_lens", ctypes.c_void_p), ("batch", ctypes.c_int32), ("max_blocks", ctypes.c_int32),
+        ("block_size", ctypes.c_int32), ("n_kv_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32),
+        ("n_blocks", ctypes.c_int64),
     ]
 
 
@@ -100,6 +112,15 @@ def lib():
         L.csa2_cp_merge_select.argtypes = [vp, i32, i32, i32, vp, i32, vp, i32, vp, vp, sz, vp]
         L.csa2_cp_sparse_swa_attn.argtypes = [cp, vp, vp, vp, i32, vp, i32, i32, ctypes.c_float, vp, vp, vp, sz, vp]
         L.csa2_lse_merge.argtypes = [i32, i32, i32, i32, vp, ctypes.c_int64, vp, ctypes.c_int64, vp, vp, vp]
+        kp, i64 = ctypes.POINTER(csa2_kv8_cache), ctypes.c_int64
+        L.csa2_kv8_workspace_bytes.restype = sz
+        L.csa2_kv8_workspace_bytes.argtypes = [kp, i32, i32, i32]
+        L.csa2_kv8_append.argtypes = [kp, vp, vp, i32, i64, i64, i32, vp, vp, vp, vp]
+        L.csa2_kv8_read.argtypes = [kp, vp, vp, i32, vp, vp, i32, vp, vp]
+        L.csa2_kv8_attn.argtypes = [kp, vp, i32, i64, i64, i32, i32, vp, i32, ctypes.c_float, vp, vp, vp, sz, vp]
+        L.csa2_kv8_select_blocks.argtypes = [kp, vp, i32, i64, i64, i32, i32, vp, i32, i32, i32, vp, vp, sz, vp]
+        L.csa2_kv8_block_attn.argtypes = [kp, vp, i32, i64, i64, i32, i32, vp, vp, i32, ctypes.c_float, vp, vp, vp, sz,
+                                          vp]
         L.csa2_read_device_status.argtypes = [vp, vp]
         L.csa2_status_string.restype = ctypes.c_char_p
         L.csa2_status_string.argtypes = [i32]
@@ -114,7 +135,8 @@ def lib():
                      "csa2_layer_step", "csa2_prefill_layer", "csa2_read_device_status",
                      "csa2_debug_set_wait_limit", "csa2_cp_index_local", "csa2_cp_reindex_local", "csa2_cp_reindex_select",
                      "csa2_cp_merge_select", "csa2_cp_sparse_swa_attn", "csa2_lse_merge",
-                     "csa2_debug_encode"):
+                     "csa2_kv8_append", "csa2_kv8_read", "csa2_kv8_attn", "csa2_kv8_select_blocks",
+                     "csa2_kv8_block_attn", "csa2_debug_encode"):
             getattr(L, name).restype = i32
         _lib = L
     return _lib
@@ -451,6 +473,228 @@ def lse_merge(outs, lses, out, lse=None, stream=None):
     _check(lib().csa2_lse_merge(R, B, H, D, ctypes.c_void_p(outs.data_ptr()), outs.stride(0),
                                 ctypes.c_void_p(lses.data_ptr()), lses.stride(0), _p(out), _p(lse), _stream(stream)),
            "lse_merge")
+
+
+# ---------------------------------------------------------------- 8-bit key / value cache
+_KV8_DTYPES = {torch.bfloat16: BF16, torch.float16: F16, torch.float32: F32}
+
+
+class KV8Cache:
+    """The 8-bit key / value cache of one grouped-query layer: E4M3 codes
+    [n_blocks, n_kv_heads, block_size, head_dim], power-of-two scales
+    [n_blocks, n_kv_heads], key bounds [n_blocks, n_kv_heads, 2, head_dim], a
+    block table [batch, max_blocks] (None: contiguous) and seq_lens [batch],
+    all on one device.  seq_lens counts the rows of the current call; the
+    caller advances it (`cache.seq_lens += n`) and nothing in the library
+    changes it."""
+
+    def __init__(self, batch, n_kv_heads, head_dim, max_blocks, seq_lens, block_size=64, n_blocks=None,
+                 block_table=None, bounds=True, device="cuda"):
+        if torch.device(device).type != "cuda":
+            raise ValueError("the cache lives in device memory; got device %s" % device)
+        n_blocks = batch * max_blocks if n_blocks is None else n_blocks
+        z = dict(device=device)
+        shape = (n_blocks, n_kv_heads)
+        self._set(torch.zeros((*shape, block_size, head_dim), dtype=torch.uint8, **z),
+                  torch.zeros((*shape, block_size, head_dim), dtype=torch.uint8, **z),
+                  torch.zeros(shape, dtype=torch.float32, **z), torch.zeros(shape, dtype=torch.float32, **z),
+                  torch.as_tensor(seq_lens, dtype=torch.int32).to(device).contiguous(),
+                  torch.zeros((*shape, 2, head_dim), dtype=torch.uint8, **z) if bounds else None,
+                  None if block_table is None else torch.as_tensor(block_table, dtype=torch.int32).to(device).contiguous(),
+                  max_blocks)
+
+    @classmethod
+    def wrap(cls, k_codes, v_codes, k_scale, v_scale, seq_lens, k_bounds=None, block_table=None, max_blocks=None):
+        """A cache over tensors the caller holds (shared, not copied)."""
+        self = cls.__new__(cls)
+        self._set(k_codes, v_codes, k_scale, v_scale, seq_lens, k_bounds, block_table, max_blocks)
+        return self
+
+    def _set(self, k, v, ks, vs, seq_lens, kb, table, max_blocks):
+        n_blocks, heads, bs, dim = k.shape
+        batch = seq_lens.numel()
+        if table is not None:
+            max_blocks = table.shape[1] if max_blocks is None else max_blocks
+            if table.dtype != torch.int32 or tuple(table.shape) != (batch, max_blocks):
+                raise ValueError("block_table is int32 [batch, max_blocks]")
+        elif max_blocks is None:
+            max_blocks = n_blocks // batch
+        for t, dt, shape, what in ((k, torch.uint8, (n_blocks, heads, bs, dim), "k_codes"),
+                                   (v, torch.uint8, (n_blocks, heads, bs, dim), "v_codes"),
+                                   (ks, torch.float32, (n_blocks, heads), "k_scale"),
+                                   (vs, torch.float32, (n_blocks, heads), "v_scale"),
+                                   (kb, torch.uint8, (n_blocks, heads, 2, dim), "k_bounds"),
+                                   (seq_lens, torch.int32, (batch,), "seq_lens")):
+            if t is not None and (t.dtype != dt or tuple(t.shape) != shape):
+                raise ValueError("%s is %s %s; got %s %s" % (what, dt, shape, t.dtype, tuple(t.shape)))
+            if t is not None and t.device != k.device:
+                raise ValueError("the cache's tensors live on one device")
+        self.k, self.v, self.k_scale, self.v_scale, self.k_bounds = k, v, ks, vs, kb
+        self.seq_lens, self.block_table = seq_lens, table
+        self.batch, self.max_blocks, self.block_size, self.n_kv_heads, self.head_dim = batch, max_blocks, bs, heads, dim
+        self.device = k.device
+        self.c = csa2_kv8_cache(_addr(k), _addr(v), _addr(ks), _addr(vs), _addr(kb), _addr(table), _addr(seq_lens),
+                                batch, max_blocks, bs, heads, dim, n_blocks)
+        self.ref = ctypes.byref(self.c)
+
+
+def _kv8_ptr(cache, t, dtype, shape, what):
+    """Address of a dense tensor of a kv8 call, on the cache's device."""
+    if t is None:
+        return None
+    if t.dtype != dtype or tuple(t.shape) != shape:
+        raise ValueError("%s is %s %s; got %s %s" % (what, dtype, shape, t.dtype, tuple(t.shape)))
+    if t.device != cache.device:
+        raise ValueError("%s is on %s, the cache on %s" % (what, t.device, cache.device))
+    if not t.is_contiguous():
+        raise ValueError("%s must be contiguous" % what)
+    return t.data_ptr()
+
+
+def _kv8_rows(cache, t, heads, what):
+    """Address and (batch, row) strides of rows [batch, T, heads, head_dim]
+    whose heads and channels are dense (a slice of a wider row is fine)."""
+    if t.dim() != 4 or t.shape[0] != cache.batch or t.shape[2] != heads or t.shape[3] != cache.head_dim:
+        raise ValueError("%s is [%d, T, %s, %d]; got %s"
+                         % (what, cache.batch, heads, cache.head_dim, tuple(t.shape)))
+    if t.device != cache.device:
+        raise ValueError("%s is on %s, the cache on %s" % (what, t.device, cache.device))
+    sb, st, sh, sd = t.stride()
+    if (sd != 1 and t.shape[3] > 1) or (sh != t.shape[3] and heads > 1):
+        raise ValueError("%s: heads and channels must be dense" % what)
+    T = t.shape[1]
+    st = st if T > 1 else 8
+    sb = sb if t.shape[0] > 1 else 8
+    if st % 8 or sb % 8:
+        raise ValueError("%s: row strides must be multiples of 8 elements" % what)
+    return t.data_ptr(), sb, st
+
+
+def _kv8_stream(cache, stream):
+    s = stream if stream is not None else torch.cuda.current_stream(cache.device)
+    return s.cuda_stream
+
+
+class _kv8_device:
+    """Launches go to the cache's device, whichever is current."""
+
+    def __new__(cls, cache):
+        i = cache.device.index
+        if i is None or torch.cuda.current_device() == i:
+            return _SAME_DEVICE
+        return torch.cuda.device(i)
+
+
+class _SameDevice:
+    def __enter__(self):
+        return self
+
+    def __exit__(self, *a):
+        return False
+
+
+_SAME_DEVICE = _SameDevice()
+
+
+def kv8_workspace_bytes(cache, T, H, n_sel=0):
+    """Bytes of workspace (a uint8 tensor, cleared once with workspace_init)
+    for T query rows of H heads and, where blocks are selected, n_sel."""
+    n = lib().csa2_kv8_workspace_bytes(cache.ref, T, H, n_sel)
+    if n == 0:
+        raise CSA2Error(ERR_INVALID_ARG, "kv8_workspace_bytes")
+    return n
+
+
+def _kv8_ws(cache, ws):
+    if ws is None:
+        return None
+    if ws.device != cache.device or not ws.is_contiguous():
+        raise ValueError("the workspace is a contiguous tensor on the cache's device")
+    return ws.data_ptr()
+
+
+def kv8_append(cache, k_new, v_new, start_pos, n_new=None, ws=None, stream=None):
+    """k_new, v_new [B, T, n_kv_heads, head_dim] bf16 / fp16 / fp32 (equal
+    strides, heads and channels dense) quantised into positions start_pos[b] +
+    j, j < n_new[b] (None: T); start_pos, n_new int32 [B].  seq_lens stays."""
+    B = cache.batch
+    if k_new.dtype not in _KV8_DTYPES or v_new.dtype != k_new.dtype or v_new.shape != k_new.shape:
+        raise ValueError("k_new and v_new are bf16, fp16 or fp32 tensors of one shape and type")
+    kp, sb, st = _kv8_rows(cache, k_new, cache.n_kv_heads, "k_new")
+    vp, vsb, vst = _kv8_rows(cache, v_new, cache.n_kv_heads, "v_new")
+    if (sb, st) != (vsb, vst):
+        raise ValueError("k_new and v_new must have equal strides")
+    i32 = torch.int32
+    with _kv8_device(cache):
+        _check(lib().csa2_kv8_append(cache.ref, kp, vp, _KV8_DTYPES[k_new.dtype], sb, st, k_new.shape[1],
+                                     _kv8_ptr(cache, start_pos, i32, (B,), "start_pos"),
+                                     _kv8_ptr(cache, n_new, i32, (B,), "n_new"), _kv8_ws(cache, ws),
+                                     _kv8_stream(cache, stream)), "kv8_append")
+
+
+def kv8_read(cache, start_pos, k_out, v_out, n_rows=None, ws=None, stream=None):
+    """Positions start_pos[b] + j, j < n_rows[b] (None: T), as values into
+    k_out, v_out [B, T, n_kv_heads, head_dim] bf16 / fp16 / fp32."""
+    B, i32 = cache.batch, torch.int32
+    if k_out.dtype not in _KV8_DTYPES or k_out.dim() != 4:
+        raise ValueError("k_out and v_out are bf16, fp16 or fp32 [batch, T, n_kv_heads, head_dim]")
+    shape = (B, k_out.shape[1], cache.n_kv_heads, cache.head_dim)
+    with _kv8_device(cache):
+        _check(lib().csa2_kv8_read(cache.ref, _kv8_ptr(cache, start_pos, i32, (B,), "start_pos"),
+                                   _kv8_ptr(cache, n_rows, i32, (B,), "n_rows"), shape[1],
+                                   _kv8_ptr(cache, k_out, k_out.dtype, shape, "k_out"),
+                                   _kv8_ptr(cache, v_out, k_out.dtype, shape, "v_out"), _KV8_DTYPES[k_out.dtype],
+                                   _kv8_ws(cache, ws), _kv8_stream(cache, stream)), "kv8_read")
+
+
+def _kv8_query(cache, q):
+    if q.dtype not in (torch.bfloat16, torch.float16):
+        raise ValueError("q is bf16 or fp16; got %s" % q.dtype)
+    if q.dim() != 4:
+        raise ValueError("q is [batch, T, H, head_dim]")
+    qp, sb, st = _kv8_rows(cache, q, q.shape[2], "q")
+    return qp, _KV8_DTYPES[q.dtype], sb, st, q.shape[1], q.shape[2]
+
+
+def kv8_attn(cache, q, out, ws, lse=None, window=0, n_q=None, sm_scale=0.0, stream=None):
+    """Causal attention of q [B, T, H, head_dim] (bf16 / fp16, row j of
+    sequence b at seq_lens[b] - n_q[b] + j; n_q None: T) over the cache into
+    out (q's shape and type) and lse fp32 [B, T, H].  window > 0: the last
+    `window` positions only."""
+    qp, dt, sb, st, T, H = _kv8_query(cache, q)
+    B = cache.batch
+    with _kv8_device(cache):
+        _check(lib().csa2_kv8_attn(cache.ref, qp, dt, sb, st, T, H, _kv8_ptr(cache, n_q, torch.int32, (B,), "n_q"),
+                                   window, sm_scale, _kv8_ptr(cache, out, q.dtype, (B, T, H, cache.head_dim), "out"),
+                                   _kv8_ptr(cache, lse, torch.float32, (B, T, H), "lse"), _kv8_ws(cache, ws),
+                                   ws.numel() * ws.element_size(), _kv8_stream(cache, stream)), "kv8_attn")
+
+
+def kv8_select_blocks(cache, q, block_idx, ws, n_first=0, n_recent=1, n_q=None, stream=None):
+    """The blocks every query row's key heads attend to, by the key bounds:
+    block_idx int32 [B, T, n_kv_heads, n_sel], ascending, -1 last; the first
+    n_first and the newest n_recent visible blocks are always among them."""
+    qp, dt, sb, st, T, H = _kv8_query(cache, q)
+    B, n_sel = cache.batch, block_idx.shape[-1]
+    with _kv8_device(cache):
+        _check(lib().csa2_kv8_select_blocks(
+            cache.ref, qp, dt, sb, st, T, H, _kv8_ptr(cache, n_q, torch.int32, (B,), "n_q"), n_sel, n_first, n_recent,
+            _kv8_ptr(cache, block_idx, torch.int32, (B, T, cache.n_kv_heads, n_sel), "block_idx"), _kv8_ws(cache, ws),
+            ws.numel() * ws.element_size(), _kv8_stream(cache, stream)), "kv8_select_blocks")
+
+
+def kv8_block_attn(cache, q, block_idx, out, ws, lse=None, n_q=None, sm_scale=0.0, stream=None):
+    """kv8_attn over the listed blocks alone (block_idx as kv8_select_blocks
+    writes it)."""
+    qp, dt, sb, st, T, H = _kv8_query(cache, q)
+    B, n_sel = cache.batch, block_idx.shape[-1]
+    with _kv8_device(cache):
+        _check(lib().csa2_kv8_block_attn(
+            cache.ref, qp, dt, sb, st, T, H, _kv8_ptr(cache, n_q, torch.int32, (B,), "n_q"),
+            _kv8_ptr(cache, block_idx, torch.int32, (B, T, cache.n_kv_heads, n_sel), "block_idx"), n_sel, sm_scale,
+            _kv8_ptr(cache, out, q.dtype, (B, T, H, cache.head_dim), "out"),
+            _kv8_ptr(cache, lse, torch.float32, (B, T, H), "lse"), _kv8_ws(cache, ws),
+            ws.numel() * ws.element_size(), _kv8_stream(cache, stream)), "kv8_block_attn")
 
 
 def debug_encode(x, codes, fmt, stream=None):

@@ -807,6 +807,7 @@ csa2_status csa2_read_device_status(void* ws, void* stream) {
     if (cudaStreamSynchronize(st) != cudaSuccess) return CSA2_ERR_CUDA;
     if (word & kStatusTimeout) return CSA2_ERR_TIMEOUT;
     if (word & kStatusBounds) return CSA2_ERR_DEVICE_BOUNDS;
+    if (word & kStatusNonFinite) return CSA2_ERR_NONFINITE;
     return CSA2_OK;
 }
 
@@ -835,6 +836,7 @@ const char* csa2_status_string(csa2_status s) {
         case CSA2_ERR_CUDA: return "CSA2_ERR_CUDA";
         case CSA2_ERR_TIMEOUT: return "CSA2_ERR_TIMEOUT";
         case CSA2_ERR_DEVICE_BOUNDS: return "CSA2_ERR_DEVICE_BOUNDS";
+        case CSA2_ERR_NONFINITE: return "CSA2_ERR_NONFINITE";
     }
     return "CSA2_UNKNOWN_STATUS";
 }

@@ -72,13 +72,14 @@ typedef enum {
     CSA2_ERR_UNSUPPORTED = 2,   /* legal shape this build does not implement */
     CSA2_ERR_CUDA = 3,          /* a CUDA runtime call or launch failed */
     CSA2_ERR_TIMEOUT = 4,       /* device: a bounded wait gave up */
-    CSA2_ERR_DEVICE_BOUNDS = 5  /* device: index / page / length out of range */
+    CSA2_ERR_DEVICE_BOUNDS = 5, /* device: index / page / length out of range */
+    CSA2_ERR_NONFINITE = 6      /* device: a row to be quantised held an infinity or a NaN (csa2_kv8_append) */
 } csa2_status;
 
 /* Layer roles, [TLDR] paragraph 3. */
 typedef enum { CSA2_FULL = 0, CSA2_REINDEX = 1, CSA2_REUSE = 2 } csa2_mode;
 
-typedef enum { CSA2_F32 = 0, CSA2_BF16 = 1, CSA2_E4M3 = 2 } csa2_dtype;
+typedef enum { CSA2_F32 = 0, CSA2_BF16 = 1, CSA2_E4M3 = 2, CSA2_F16 = 3 } csa2_dtype;
 
 /*
  * The global cache shared by every layer of a stack ([HN] key point 2):
@@ -498,10 +499,153 @@ CSA2_API csa2_status csa2_lse_merge(int R, int batch, int H, int dim, const floa
                                     const float* lses, int64_t lse_stride, float* out, float* lse, void* stream);
 
 /*
+ * ---------------------------------------------------------------------------
+ * Layers with keys and values of their own: an 8-bit cache for grouped-query
+ * attention, the attention that reads it, and attention over blocks chosen by
+ * a cheap score.  A serving stack uses it for the layers that do not share the
+ * latent cache above.  The pages describe no such layer; formats and rules are
+ * this library's.
+ *
+ *   k_codes, v_codes  [n_blocks][n_kv_heads][block_size][head_dim] E4M3 bytes
+ *   k_scale, v_scale  [n_blocks][n_kv_heads] fp32, each a power of two: a code
+ *                     stands for value(code) * scale
+ *   k_bounds          [n_blocks][n_kv_heads][2][head_dim] E4M3, or NULL: per
+ *                     channel a lower and an upper bound of the block's key
+ *                     codes in whole units of k_scale (csa2_kv8_select_blocks
+ *                     needs them, csa2_kv8_append keeps them)
+ *   block_table       [batch][max_blocks] int32 physical block ids, or NULL
+ *                     for the contiguous layout (block i of sequence b is
+ *                     block b * max_blocks + i)
+ *   seq_lens          [batch] int32, valid positions of each sequence, with
+ *                     the rows of the current call; read on the device
+ *
+ * head_dim 64 or 128; block_size 16, 32, 64 or 128; n_kv_heads * 2 <= 65535;
+ * n_blocks * n_kv_heads * block_size < 2^31; max_blocks * block_size <= 2^30.
+ * Pointers are 16-byte aligned, except block_table, seq_lens, the scales and
+ * per-sequence int32 arrays (4-byte).  Distinct sequences own distinct blocks
+ * that they write to; blocks that are only read may be shared.
+ *
+ * Rows of a call are [batch][T]: row j of sequence b lies at b * stride_b +
+ * j * stride_t (in elements; heads and channels are dense behind it, so a
+ * slice of a fused projection needs no copy; both strides are multiples of 8).
+ * A padded batch gives n (device int32 [batch], 0 <= n[b] <= T): only rows
+ * j < n[b] are read, and what an output holds for the others stays as it was.
+ * n == NULL means T rows of every sequence.
+ *
+ * Query row j of sequence b sits at position p = seq_lens[b] - n[b] + j and
+ * sees positions t <= p.  H query heads, a multiple of n_kv_heads: head h reads
+ * key head h / (H / n_kv_heads).
+ */
+typedef struct {
+    uint8_t* k_codes;
+    uint8_t* v_codes;
+    float* k_scale;
+    float* v_scale;
+    uint8_t* k_bounds;
+    const int32_t* block_table;
+    const int32_t* seq_lens;
+    int32_t batch;
+    int32_t max_blocks;
+    int32_t block_size;
+    int32_t n_kv_heads;
+    int32_t head_dim;
+    int64_t n_blocks;
+} csa2_kv8_cache;
+
+/*
+ * Bytes of workspace for the kv8 calls with T query rows of H heads and, where
+ * blocks are selected, n_sel of them (0: none).  0 on invalid arguments.
+ * Cleared once with csa2_workspace_init; calls on one stream may share it.
+ */
+CSA2_API size_t csa2_kv8_workspace_bytes(const csa2_kv8_cache* cache, int T, int H, int n_sel);
+
+/*
+ * Quantise-on-append: rows k_new, v_new [batch][T][n_kv_heads][head_dim] of
+ * dtype (CSA2_BF16, CSA2_F16 or CSA2_F32; both with these strides) become
+ * positions start_pos[b] + j, j < n_new[b].  Per block and head, for keys and
+ * values apart, with x over the block's new rows:
+ *     s    = the least 2^e, -120 <= e <= 120, with max |x| <= 448 s,
+ *     code = E4M3 round-to-nearest-even (x / s).
+ * A block that holds rows before the call (start_pos inside it) gets the
+ * larger of its scale and s; when that is larger than its own, the held codes
+ * become E4M3 round-to-nearest-even (value * s_old / s_new).  k_bounds: floor
+ * of the least and ceil of the greatest new code value per channel, joined
+ * with the held ones (value * s_old / s_new, rounded outward).  After a
+ * sequence was cut back and appended to again the bounds of its last block
+ * still cover the dropped rows.  A block is taken to hold exactly the
+ * positions before start_pos; what it held behind them is overwritten or left.
+ * The call does not change seq_lens.  Rows must be finite: an infinity is
+ * stored as +-448 s, a NaN as 0, neither counts for s, and either sets
+ * CSA2_ERR_NONFINITE in ws; positions outside the cache are skipped and set
+ * CSA2_ERR_DEVICE_BOUNDS (ws nullable, only its status word is used).
+ * (T + block_size) rounded up to blocks times n_kv_heads is the grid: T up to
+ * 2^30.
+ */
+CSA2_API csa2_status csa2_kv8_append(const csa2_kv8_cache* cache, const void* k_new, const void* v_new,
+                                     csa2_dtype dtype, int64_t stride_b, int64_t stride_t, int T,
+                                     const int32_t* start_pos, const int32_t* n_new, void* ws, void* stream);
+
+/*
+ * Rows back as values: k_out, v_out [batch][T][n_kv_heads][head_dim] (dense, of
+ * dtype) <- value(code) * scale of positions start_pos[b] + j, j < n_rows[b],
+ * rounded once.  A position outside the cache is written as zeros and sets
+ * CSA2_ERR_DEVICE_BOUNDS in ws (nullable).
+ */
+CSA2_API csa2_status csa2_kv8_read(const csa2_kv8_cache* cache, const int32_t* start_pos, const int32_t* n_rows,
+                                   int T, void* k_out, void* v_out, csa2_dtype dtype, void* ws, void* stream);
+
+/*
+ * Attention over the cache: for query row (b, j, h) at p, over the visible
+ * positions t in [max(0, p - window + 1), p] (window == 0: [0, p]),
+ *     z_t = sm_scale q . k_t        (sm_scale <= 0: 1 / sqrt(head_dim))
+ *     out = sum_t softmax(z)_t v_t  [batch][T][H][head_dim] of the query's type
+ *     lse = log sum_t exp(z_t)      fp32 [batch][T][H], nullable
+ * q is CSA2_BF16 or CSA2_F16.  A row that sees nothing (p < 0) gives out = 0,
+ * lse = -inf.  The products take q and the codes as they are and accumulate in
+ * fp32; the weights exp(z - max) are rounded to fp16 for the second product,
+ * sums and lse use them unrounded.  What a block holds behind the sequence's
+ * end does not enter, whatever it is.
+ */
+CSA2_API csa2_status csa2_kv8_attn(const csa2_kv8_cache* cache, const void* q, csa2_dtype q_dtype, int64_t stride_b,
+                                   int64_t stride_t, int T, int H, const int32_t* n_q, int window, float sm_scale,
+                                   void* out, float* lse, void* ws, size_t ws_bytes, void* stream);
+
+/*
+ * The blocks each query row's key heads attend to.  For (b, j, key head h) the
+ * blocks 0 .. p / block_size are visible; block_idx[b][j][h][0..n_sel) <- the
+ * min(n_sel, visible) chosen ones in ascending order, then -1: the first
+ * n_first and the newest n_recent visible blocks always, the others by the
+ * score, equal scores by the lower index.  The score of a block of scale s,
+ * bounds lo, hi is the greatest, over the query heads of h, of
+ *     2^e s sum_d (min(qi_d, 0) lo_d + max(qi_d, 0) hi_d),
+ * qi = round-to-nearest-even(q 2^-e), e the least with max |q| <= 127 * 2^e
+ * (-118 <= e; channels that are not finite count as 0): an upper bound of
+ * every q . k in the block, up to the rounding of q.  The sums are exact.
+ * Bounds cover what the block holds at the time of the call, rows behind p
+ * included.  1 <= n_sel <= 2048, n_first + n_recent <= n_sel.
+ */
+CSA2_API csa2_status csa2_kv8_select_blocks(const csa2_kv8_cache* cache, const void* q, csa2_dtype q_dtype,
+                                            int64_t stride_b, int64_t stride_t, int T, int H, const int32_t* n_q,
+                                            int n_sel, int n_first, int n_recent, int32_t* block_idx, void* ws,
+                                            size_t ws_bytes, void* stream);
+
+/*
+ * csa2_kv8_attn over the positions t <= p of the blocks listed in
+ * block_idx[b][j][h / (H / n_kv_heads)][0..n_sel) alone: strictly ascending
+ * visible blocks, then -1 (as csa2_kv8_select_blocks writes them).  An entry
+ * that breaks this sets CSA2_ERR_DEVICE_BOUNDS, and the call's results are not
+ * to be used.  n_sel >= 1.
+ */
+CSA2_API csa2_status csa2_kv8_block_attn(const csa2_kv8_cache* cache, const void* q, csa2_dtype q_dtype,
+                                         int64_t stride_b, int64_t stride_t, int T, int H, const int32_t* n_q,
+                                         const int32_t* block_idx, int n_sel, float sm_scale, void* out, float* lse,
+                                         void* ws, size_t ws_bytes, void* stream);
+
+/*
  * Synchronise `stream`, then return the sticky device status recorded in the
- * workspace (CSA2_OK, CSA2_ERR_DEVICE_BOUNDS or CSA2_ERR_TIMEOUT; the first
- * error class found in that order of severity: TIMEOUT, then BOUNDS) and clear
- * it.  Returns CSA2_ERR_CUDA if the synchronisation or copy fails.
+ * workspace (CSA2_OK, CSA2_ERR_DEVICE_BOUNDS, CSA2_ERR_NONFINITE or
+ * CSA2_ERR_TIMEOUT; the first error class found in that order of severity:
+ * TIMEOUT, then BOUNDS, then NONFINITE) and clear it.  Returns CSA2_ERR_CUDA if the synchronisation or copy fails.
  */
 CSA2_API csa2_status csa2_read_device_status(void* ws, void* stream);
 
