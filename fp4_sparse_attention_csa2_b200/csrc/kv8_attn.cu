@@ -6,16 +6,21 @@
 // and head) and its work is moving them: the codes go by TMA into a ring of
 // each warp's own (no synchronisation between warps while they stream; the
 // rows swizzled, so that the loads below are free of bank conflicts), from
-// there as 16-byte loads straight into the operand layout of mma.m16n8k16,
-// converted to fp16 by bit placement (exact).  The layouts need no
-// transposition: a product's k order may be permuted as long as both operands
-// agree, so a lane's 16 bytes of a key row are four k steps, and the
-// probabilities leave the first product in the layout the second one reads.
-// tcgen05 would take the codes as they are (kind::f8f6f4) but wants the
-// probabilities as E4M3 terms and 128 rows a tile; with at most 32 rows it
-// has nothing to win over a kernel that already waits for HBM.
+// there as 16-byte loads into the operand layout of mma.m16n8k16, converted to
+// fp16 two at a time (exact).
 //
-// Work split: a step is 64 positions of one (sequence, head, row tile); the
+// Both products are taken transposed, S^T = K Q^T and O^T = V^T P^T: positions
+// and channels fill the 16 rows of a tile and the query rows its 8 columns, so
+// that the usual group of up to 8 query heads wastes nothing.  No operand is
+// transposed in memory: the order of a product's k index may be permuted as
+// long as both operands agree, so a lane's 16 bytes of a key row are four k
+// steps, and of a value row the same channel of two positions is one byte
+// permutation; the weights turn around in registers (movmatrix).
+// tcgen05 would take the codes as they are (kind::f8f6f4) but wants the
+// weights as E4M3 terms and 128 rows a tile; with at most 32 rows it has
+// nothing to win over a kernel that already waits for HBM.
+//
+// Work split: a step is 128 positions of one (sequence, head, row tile); the
 // steps of the whole batch form one line, which the CTAs cut into equal
 // pieces (the lengths are on the device, so every CTA sums them itself).  A
 // CTA finishes what lies inside its piece; an item that is cut leaves
@@ -32,7 +37,8 @@ namespace csa2 {
 namespace {
 
 constexpr int kWarps = 4, kThreads = kWarps * 32;
-constexpr int kTile = 16;                 // positions a warp takes at a time
+constexpr int kGroup = 16;                // positions of one matrix tile
+constexpr int kTile = 2 * kGroup;         // positions a warp takes at a time
 constexpr int kStep = kWarps * kTile;     // positions a CTA takes at a time
 constexpr float kNone = -3.0e38f;         // running maximum before any position
 // Weights are 2^(z - M + 8) in fp16: the greatest is a power of two (exact, so
@@ -57,23 +63,23 @@ struct Cursor {
     int steps, tiles, L, n, lo;
 };
 
-template <int MT, bool LIST>
+template <int NT, bool LIST>
 struct Work {
     const Params& p;
     __device__ explicit Work(const Params& p) : p(p) {}
 
     // Rows of item k, and the (token, head of the group) of its row i.
     __device__ __forceinline__ int rows(const Cursor& k) const {
-        const int left = LIST ? p.G - k.rt % p.gt * 16 * MT : k.n * p.G - k.rt * 16 * MT;
-        return left < 16 * MT ? left : 16 * MT;
+        const int left = LIST ? p.G - k.rt % p.gt * 8 * NT : k.n * p.G - k.rt * 8 * NT;
+        return left < 8 * NT ? left : 8 * NT;
     }
     __device__ __forceinline__ int2 token(const Cursor& k, int i) const {
         if (LIST) {
             const int j = k.rt / p.gt;
-            return make_int2(j, (k.rt - j * p.gt) * 16 * MT + i);
+            return make_int2(j, (k.rt - j * p.gt) * 8 * NT + i);
         }
-        const int j = (k.rt * 16 * MT + i) / p.G;
-        return make_int2(j, k.rt * 16 * MT + i - j * p.G);
+        const int j = (k.rt * 8 * NT + i) / p.G;
+        return make_int2(j, k.rt * 8 * NT + i - j * p.G);
     }
     // The shape of sequence b's items.
     __device__ __forceinline__ void load(Cursor& k, int b, uint32_t* status) const {
@@ -95,7 +101,7 @@ struct Work {
                 k.lo = first > 0 ? (int)first / kTile * kTile : 0;
             }
             k.steps = (k.L - k.lo + kStep - 1) / kStep;
-            k.tiles = (k.n * p.G + 16 * MT - 1) / (16 * MT);
+            k.tiles = (k.n * p.G + 8 * NT - 1) / (8 * NT);
         }
         if (k.steps < 1) k.steps = 1;  // an empty row still has to be written
     }
@@ -122,8 +128,8 @@ struct Work {
 // The line of all steps: its length, and the sequence that holds step u with
 // the steps before it.  Every thread of the CTA calls it; `sums` is kThreads + 1
 // words of shared memory.
-template <int MT, bool LIST>
-__device__ int64_t line_sums(const Work<MT, LIST>& w, int64_t* sums, uint32_t* status) {
+template <int NT, bool LIST>
+__device__ int64_t line_sums(const Work<NT, LIST>& w, int64_t* sums, uint32_t* status) {
     const int tid = threadIdx.x, nb = w.p.c.batch, per = (nb + kThreads - 1) / kThreads;
     int64_t s = 0;
     for (int i = 0; i < per; ++i) {
@@ -152,8 +158,8 @@ __device__ int64_t line_sums(const Work<MT, LIST>& w, int64_t* sums, uint32_t* s
 }
 
 // The step u (0 <= u < total) as a cursor.
-template <int MT, bool LIST>
-__device__ void line_find(const Work<MT, LIST>& w, const int64_t* sums, int64_t u, Cursor& k) {
+template <int NT, bool LIST>
+__device__ void line_find(const Work<NT, LIST>& w, const int64_t* sums, int64_t u, Cursor& k) {
     const int nb = w.p.c.batch, per = (nb + kThreads - 1) / kThreads;
     int lo = 0, hi = kThreads;  // sums[lo] <= u < sums[hi]
     while (hi - lo > 1) {
@@ -172,25 +178,23 @@ __device__ void line_find(const Work<MT, LIST>& w, const int64_t* sums, int64_t 
     w.seek(k, u);
 }
 
-// How many CTAs share `total` steps: all, but no fewer than two steps each.
+// How many CTAs share `total` steps.
 __device__ __forceinline__ int64_t sharing(int64_t total, int ctas) {
-    const int64_t most = (total + 1) / 2;
-    return most < ctas ? (most < 1 ? 1 : most) : ctas;
+    return total < ctas ? (total < 1 ? 1 : total) : ctas;
 }
 
-template <int D, int MT>
+template <int D, int NT>
 struct Smem {
     static constexpr int kRows = kTile * D;          // bytes of one tile's keys (or values)
-    // three CTAs an SM with one row tile, two with two: 2 or more tiles in flight a warp
-    static constexpr int kStages = (MT == 1 ? 3 : 5) * (128 / D);
-    static constexpr int kNt = D / 8;
+    // a warp computes on one stage while the others fill: two are enough with three CTAs an SM
+    static constexpr int kStages = (NT <= 2 ? 2 : 3) * (128 / D);
     static constexpr int ring = 0;                                            // [warp][stage][K, V]
-    static constexpr int merge = ring + kWarps * kStages * 2 * kRows;         // [warp][2][kNt][32] floats
-    static constexpr int stats = merge + kWarps * 2 * kNt * 32 * 4;           // [warp][16 * MT][3] floats
-    static constexpr int slots = stats + kWarps * 16 * MT * 3 * 4;            // [warp][stage] int2
-    static constexpr int bars = slots + kWarps * kStages * 8;                 // [warp][stage]
-    static constexpr int sums = bars + kWarps * kStages * 8;                  // kThreads + 1
-    static constexpr int bytes = sums + (kThreads + 1) * 8 + 1024;            // base aligned to 1024
+    static constexpr int merge = ring + kWarps * kStages * 2 * kRows;         // [warp][16][32] floats
+    static constexpr int stats = merge + kWarps * 16 * 32 * 4;                // [warp][8 * NT][3] floats
+    static constexpr int slots = stats + kWarps * 8 * NT * 3 * 4;             // [warp][stage] int4
+    static constexpr int bars = slots + kWarps * kStages * 16;                // [warp][stage]
+    static constexpr int sums = merge;                                        // kThreads + 1 words, before the first merge
+    static constexpr int bytes = bars + kWarps * kStages * 8 + 1024;          // base aligned to 1024
 };
 
 // Partial of a cut item: [32 rows][D] outputs, per row (m, l, M), then what
@@ -200,12 +204,11 @@ struct Part {
     static constexpr int kStats = 32 * D, kDesc = kStats + 32 * 3, kFloats = kDesc + 32;
 };
 
-// N adjacent outputs x * f, rounded once to the query's type.
-template <int N>
+// Four adjacent outputs x * f, rounded once to the query's type.
 __device__ __forceinline__ void store_out(void* out, int is_bf16, int64_t at, const float* x, float f) {
-    uint32_t w[N / 2];
+    uint32_t w[2];
 #pragma unroll
-    for (int i = 0; i < N / 2; ++i) {
+    for (int i = 0; i < 2; ++i) {
         if (is_bf16) {
             const __nv_bfloat162 h = __floats2bfloat162_rn(x[2 * i] * f, x[2 * i + 1] * f);
             memcpy(&w[i], &h, 4);
@@ -215,32 +218,51 @@ __device__ __forceinline__ void store_out(void* out, int is_bf16, int64_t at, co
         }
     }
     uint16_t* dst = static_cast<uint16_t*>(out) + at;
-    if (N == 8) *reinterpret_cast<uint4*>(dst) = make_uint4(w[0], w[1], w[N / 2 - 2], w[N / 2 - 1]);
-    else *reinterpret_cast<uint2*>(dst) = make_uint2(w[0], w[1]);
+    *reinterpret_cast<uint2*>(dst) = make_uint2(w[0], w[1]);
 }
 
-template <int D, int MT, bool LIST>
-__global__ void __launch_bounds__(kThreads, MT == 1 ? 3 : 2) k_kv8_attn(const __grid_constant__ Params p,
-                                                                         const __grid_constant__ CUtensorMap kmap,
-                                                                         const __grid_constant__ CUtensorMap vmap) {
-    using S = Smem<D, MT>;
+// Two E4M3 codes in the low (high) half of w -> half2; exact.
+__device__ __forceinline__ uint32_t half2_lo(uint32_t w) {
+    uint32_t r;
+    asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, l;\n\t}" : "=r"(r) : "r"(w));
+    return r;
+}
+__device__ __forceinline__ uint32_t half2_hi(uint32_t w) {
+    uint32_t r;
+    asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, h;\n\t}" : "=r"(r) : "r"(w));
+    return r;
+}
+
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
+    uint32_t r;
+    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
+    return r;
+}
+
+// NT: tiles of eight query rows.
+template <int D, int NT, bool LIST>
+__global__ void __launch_bounds__(kThreads, NT <= 2 ? 3 : 2) k_kv8_attn(const __grid_constant__ Params p,
+                                                                        const __grid_constant__ CUtensorMap kmap,
+                                                                        const __grid_constant__ CUtensorMap vmap) {
+    using S = Smem<D, NT>;
     constexpr int kChunks = D / 64;   // 16-byte chunks of a key row per lane
-    constexpr int kNt = D / 8;        // n tiles of the second product; a lane's bytes of a value row
+    constexpr int kCh = D / 8;        // channels of a value row per lane
     constexpr int kStages = S::kStages;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = smem_raw + ((1024u - (tc::smem_u32(smem_raw) & 1023u)) & 1023u);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, r = lane >> 2, c = lane & 3;
     uint8_t* ring = smem + S::ring + warp * kStages * 2 * S::kRows;
-    int2* slots = reinterpret_cast<int2*>(smem + S::slots) + warp * kStages;
+    int4* slots = reinterpret_cast<int4*>(smem + S::slots) + warp * kStages;
     uint64_t* bars = reinterpret_cast<uint64_t*>(smem + S::bars) + warp * kStages;
     int64_t* sums = reinterpret_cast<int64_t*>(smem + S::sums);
     const int bs = p.c.bs(), G = p.G, T = p.a.q.T, H = p.a.q.H;
+    const bool pairs = bs == kGroup;  // a tile is two blocks
     if (lane == 0) {
         for (int i = 0; i < kStages; ++i) tc::mbar_init(bars + i, 1);
         tc::fence_mbar_init();
     }
     pdl_begin();
-    const Work<MT, LIST> work(p);
+    const Work<NT, LIST> work(p);
     const int64_t total = line_sums(work, sums, blockIdx.x == 0 ? p.a.status : nullptr);
     const int64_t share = sharing(total, p.ctas);
     int* desc = reinterpret_cast<int*>(p.a.part + ((int64_t)blockIdx.x * 2 + 1) * Part<D>::kFloats + Part<D>::kDesc);
@@ -252,32 +274,34 @@ __global__ void __launch_bounds__(kThreads, MT == 1 ? 3 : 2) k_kv8_attn(const __
     Cursor cur, ahead;
     line_find(work, sums, u0, cur);
     ahead = cur;
+    __syncthreads();         // `sums` is the merge buffer's
 
     // ---- the copies: the ring runs ahead of the tiles by kStages - 1.  A
     // tile's block is looked up two tiles before its copy is issued (the list
     // entry) and one tile before (the page table), so neither load is waited for.
     int64_t ahead_u = u0;
-    int look_b, look_h, look_t0, look_lb;
-    auto peek = [&]() {      // describe the tile at `ahead`, start its list load, move on
-        look_lb = -1;
+    int look_b = 0, look_h = 0, look_row = 0, look_lb[2];
+    auto peek = [&]() {      // describe the tile at `ahead`, start its list loads, move on
+        look_lb[0] = look_lb[1] = -1;
         look_b = ahead.b;
         look_h = ahead.h;
         if (ahead_u >= u1) return;
         const int off = ahead.step * kStep + warp * kTile;
         if (LIST) {
-            const int e = off >> p.c.bs_log2;
-            look_t0 = off & (bs - 1);
-            if (e < p.a.n_sel) {
-                const int32_t* l = p.a.block_idx +
-                                   (((int64_t)ahead.b * T + ahead.rt / p.gt) * p.c.heads + ahead.h) * p.a.n_sel + e;
-                const int v = __ldg(l), prev = e ? __ldg(l - 1) : -1;
-                const int pos = ahead.L - ahead.n + ahead.rt / p.gt;
+            const int j = ahead.rt / p.gt, pos = ahead.L - ahead.n + j;
+            const int32_t* l = p.a.block_idx + (((int64_t)ahead.b * T + j) * p.c.heads + ahead.h) * p.a.n_sel;
+            look_row = off & (bs - 1);
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const int e = (off >> p.c.bs_log2) + i;
+                if ((i && !pairs) || e >= p.a.n_sel) break;
+                const int v = __ldg(l + e), prev = e ? __ldg(l + e - 1) : -1;
                 if (v >= 0) {
                     // strictly ascending, visible, nothing behind padding: anything else is skipped and flagged
                     if (pos < 0 || v > (pos >> p.c.bs_log2) || (e && v <= prev) || (e && prev < 0)) {
                         if (lane == 0) flag(p.a.status, kStatusBounds);
                     } else {
-                        look_lb = v;
+                        look_lb[i] = v;
                     }
                 } else if (v < -1 && lane == 0) {
                     flag(p.a.status, kStatusBounds);
@@ -285,37 +309,48 @@ __global__ void __launch_bounds__(kThreads, MT == 1 ? 3 : 2) k_kv8_attn(const __
             }
         } else {
             const int t = ahead.lo + off;
-            if (t < ahead.L) {
-                look_lb = t >> p.c.bs_log2;
-                look_t0 = t & (bs - 1);
-            }
+            look_row = t & (bs - 1);
+            if (t < ahead.L) look_lb[0] = t >> p.c.bs_log2;
+            if (pairs && t + kGroup < ahead.L) look_lb[1] = look_lb[0] + 1;
         }
         ++ahead_u;
         if (++ahead.step >= ahead.steps) work.next_item(ahead);
     };
-    int hand_phys = -1, hand_h = 0, hand_t0 = 0, hand_lb = 0;
-    auto lookup = [&]() {    // the page of the tile peeked at
-        hand_phys = -1;
+    int hand_h = 0, hand_row = 0, hand_lb[2], hand_phys[2];
+    auto lookup = [&]() {    // the pages of the tile peeked at
         hand_h = look_h;
-        hand_lb = look_lb;
-        hand_t0 = look_t0;
-        if (look_lb >= 0) {
-            hand_phys = kv8_block(p.c, look_b, look_lb);
-            if (hand_phys < 0 && lane == 0) flag(p.a.status, kStatusBounds);
+        hand_row = look_row;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            hand_lb[i] = look_lb[i];
+            hand_phys[i] = -1;
+            if (look_lb[i] >= 0) {
+                hand_phys[i] = kv8_block(p.c, look_b, look_lb[i]);
+                if (hand_phys[i] < 0 && lane == 0) flag(p.a.status, kStatusBounds);
+            }
         }
     };
     bool alive = true;       // false once a wait ran out: no further copies, no further results
-    uint32_t issued = 0;     // copies by slot still to be waited for (bit mask)
+    uint32_t late = 0;       // slots whose copies were given up on (bit mask)
     auto issue = [&](int slot) {
         if (lane == 0) {
-            int2 d = make_int2(-1, 0);
-            if (hand_phys >= 0 && alive) {
-                const int64_t unit = (int64_t)hand_phys * p.c.heads + hand_h;
-                const int row = (int)((unit << p.c.bs_log2) + hand_t0);
-                tc::mbar_arrive_expect_tx(bars + slot, 2 * S::kRows);
-                tc::tma_load_2d(ring + slot * 2 * S::kRows, &kmap, 0, row, bars + slot);
-                tc::tma_load_2d(ring + slot * 2 * S::kRows + S::kRows, &vmap, 0, row, bars + slot);
-                d = make_int2((int)unit, (hand_lb << p.c.bs_log2) + hand_t0);
+            // (unit, first position) of both groups of 16; unit = physical block * heads + head, -1: nothing there
+            int4 d = make_int4(-1, 0, -1, 0);
+            if (alive && (hand_phys[0] >= 0 || hand_phys[1] >= 0)) {
+                uint8_t* kd = ring + slot * 2 * S::kRows;
+                const int n = pairs ? (hand_phys[0] >= 0) + (hand_phys[1] >= 0) : 2;   // groups that arrive
+                tc::mbar_arrive_expect_tx(bars + slot, n * S::kRows);
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    if (hand_phys[i] < 0) continue;
+                    const int unit = hand_phys[i] * p.c.heads + hand_h;
+                    const int row = (unit << p.c.bs_log2) + hand_row;
+                    tc::tma_load_2d(kd + i * kGroup * D, &kmap, 0, row, bars + slot);
+                    tc::tma_load_2d(kd + S::kRows + i * kGroup * D, &vmap, 0, row, bars + slot);
+                    if (i == 0) d.x = unit, d.y = (hand_lb[0] << p.c.bs_log2) + hand_row;
+                    else d.z = unit, d.w = hand_lb[1] << p.c.bs_log2;
+                }
+                if (!pairs) d.z = d.x, d.w = d.y + kGroup;
             }
             slots[slot] = d;
         }
@@ -333,9 +368,15 @@ __global__ void __launch_bounds__(kThreads, MT == 1 ? 3 : 2) k_kv8_attn(const __
     __syncwarp();
     int slot = 0;
     uint32_t phase = 0;      // parity of each slot's barrier (bit mask)
-    int2 here = slots[0];
-    float ks = here.x >= 0 ? __ldg(p.c.k_scale + here.x) : 0.0f;
-    float vs = here.x >= 0 ? __ldg(p.c.v_scale + here.x) : 0.0f;
+    int4 here = slots[0];
+    float ks[2], vs[2];      // scales of the tile's groups
+    auto scales = [&]() {
+        ks[0] = here.x >= 0 ? __ldg(p.c.k_scale + here.x) : 0.0f;
+        vs[0] = here.x >= 0 ? __ldg(p.c.v_scale + here.x) : 1.0f;
+        ks[1] = here.z >= 0 ? __ldg(p.c.k_scale + here.z) : 0.0f;
+        vs[1] = here.z >= 0 ? __ldg(p.c.v_scale + here.z) : 1.0f;
+    };
+    scales();
 
     int64_t u = u0;
     while (u < u1) {
@@ -345,226 +386,273 @@ __global__ void __launch_bounds__(kThreads, MT == 1 ? 3 : 2) k_kv8_attn(const __
         const bool to_end = todo == item_left;
         const int rows = work.rows(cur);
 
-        // ---- the query rows of this lane (r and r + 8 of every row tile) in operand layout
-        uint32_t qa[MT][kChunks * 4][4];
-        float zs[MT][2];     // factor from the product to a base-2 logit, without the key scale
-        int pos[MT][2];      // position of the row's token (-1: no row)
+        // ---- query row r of every tile of eight, in operand layout
+        uint32_t qb[NT][kChunks * 4][2];
+        float zs[NT][2];     // rows 2c, 2c + 1: factor from the product to a base-2 logit, without the key scale
+        int pos[NT][2];      // and the position of their token (-1: no row)
 #pragma unroll
-        for (int mt = 0; mt < MT; ++mt)
+        for (int nt = 0; nt < NT; ++nt) {
+            const int row = nt * 8 + r;
+            const bool ok = row < rows;
+            const int2 jg = work.token(cur, row);
+            uint32_t raw[kChunks][8];
+            const uint16_t* src = static_cast<const uint16_t*>(p.a.q.q) + (int64_t)cur.b * p.a.q.stride_b +
+                                  (int64_t)jg.x * p.a.q.stride_t + (int64_t)(cur.h * G + jg.y) * D;
 #pragma unroll
-            for (int half = 0; half < 2; ++half) {
-                const int row = mt * 16 + half * 8 + r;
-                const bool ok = row < rows;
-                const int2 jg = work.token(cur, row);
-                pos[mt][half] = ok ? cur.L - cur.n + jg.x : -1;
-                uint32_t raw[kChunks][8];
-                const uint16_t* src = static_cast<const uint16_t*>(p.a.q.q) + (int64_t)cur.b * p.a.q.stride_b +
-                                      (int64_t)jg.x * p.a.q.stride_t + (int64_t)(cur.h * G + jg.y) * D;
-#pragma unroll
-                for (int k = 0; k < kChunks; ++k) {
-                    uint4 x = make_uint4(0, 0, 0, 0), y = x;
-                    if (ok) {
-                        const uint4* s4 = reinterpret_cast<const uint4*>(src + (c * kChunks + k) * 16);
-                        x = __ldg(s4);
-                        y = __ldg(s4 + 1);
-                    }
-                    raw[k][0] = x.x, raw[k][1] = x.y, raw[k][2] = x.z, raw[k][3] = x.w;
-                    raw[k][4] = y.x, raw[k][5] = y.y, raw[k][6] = y.z, raw[k][7] = y.w;
+            for (int k = 0; k < kChunks; ++k) {
+                uint4 x = make_uint4(0, 0, 0, 0), y = x;
+                if (ok) {
+                    const uint4* s4 = reinterpret_cast<const uint4*>(src + (c * kChunks + k) * 16);
+                    x = __ldg(s4);
+                    y = __ldg(s4 + 1);
                 }
-                float back = 1.0f;
-                if (p.a.q.is_bf16) {
-                    // bf16 -> fp16: the row scaled by the power of two that takes its greatest finite
-                    // magnitude to [2^14, 2^15), so that its eight bits survive down to 2^-28 of it
-                    float amax = 0.0f;
-#pragma unroll
-                    for (int k = 0; k < kChunks; ++k)
-#pragma unroll
-                        for (int i = 0; i < 8; ++i) {
-                            const float a = fabsf(__uint_as_float(raw[k][i] << 16));
-                            const float b = fabsf(__uint_as_float(raw[k][i] & 0xFFFF0000u));
-                            if (a <= 3.4028235e38f) amax = fmaxf(amax, a);
-                            if (b <= 3.4028235e38f) amax = fmaxf(amax, b);
-                        }
-                    amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, 1));
-                    amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, 2));
-                    int e = 14 - ((int)(__float_as_uint(amax) >> 23) - 127);
-                    e = e > 126 ? 126 : e;
-                    const float up = exp2_int(e);
-                    back = exp2_int(-e);
-#pragma unroll
-                    for (int k = 0; k < kChunks; ++k)
-#pragma unroll
-                        for (int i = 0; i < 8; ++i) {
-                            const __half2 h = __floats2half2_rn(__uint_as_float(raw[k][i] << 16) * up,
-                                                                __uint_as_float(raw[k][i] & 0xFFFF0000u) * up);
-                            memcpy(&raw[k][i], &h, 4);
-                        }
-                }
-                // 2^8: what the codes' bit placement leaves out
-                zs[mt][half] = back * 256.0f * p.a.sm_scale * 1.4426950408889634f;
+                raw[k][0] = x.x, raw[k][1] = x.y, raw[k][2] = x.z, raw[k][3] = x.w;
+                raw[k][4] = y.x, raw[k][5] = y.y, raw[k][6] = y.z, raw[k][7] = y.w;
+            }
+            float back = 1.0f;
+            if (p.a.q.is_bf16) {
+                // bf16 -> fp16: the row scaled by the power of two that takes its greatest finite
+                // magnitude to [2^14, 2^15), so that its eight bits survive down to 2^-28 of it
+                float amax = 0.0f;
 #pragma unroll
                 for (int k = 0; k < kChunks; ++k)
 #pragma unroll
-                    for (int s = 0; s < 4; ++s) {  // k step s: channels 4s, 4s+2 | 4s+1, 4s+3 of the chunk
-                        const uint32_t w0 = raw[k][2 * s], w1 = raw[k][2 * s + 1];
-                        qa[mt][k * 4 + s][half] = __byte_perm(w0, w1, 0x5410);
-                        qa[mt][k * 4 + s][2 + half] = __byte_perm(w0, w1, 0x7632);
+                    for (int i = 0; i < 8; ++i) {
+                        const float a = fabsf(__uint_as_float(raw[k][i] << 16));
+                        const float b = fabsf(__uint_as_float(raw[k][i] & 0xFFFF0000u));
+                        if (a <= 3.4028235e38f) amax = fmaxf(amax, a);
+                        if (b <= 3.4028235e38f) amax = fmaxf(amax, b);
+                    }
+                amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, 1));
+                amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, 2));
+                int e = 14 - ((int)(__float_as_uint(amax) >> 23) - 127);
+                e = e > 126 ? 126 : e;
+                const float up = exp2_int(e);
+                back = exp2_int(-e);
+#pragma unroll
+                for (int k = 0; k < kChunks; ++k)
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        const __half2 h = __floats2half2_rn(__uint_as_float(raw[k][i] << 16) * up,
+                                                            __uint_as_float(raw[k][i] & 0xFFFF0000u) * up);
+                        memcpy(&raw[k][i], &h, 4);
                     }
             }
+            const float z = back * p.a.sm_scale * 1.4426950408889634f;
+            const int pr = ok ? cur.L - cur.n + jg.x : -1;
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {   // row 2c + e is held by the lanes with r = 2c + e
+                zs[nt][e] = __shfl_sync(0xFFFFFFFFu, z, (2 * c + e) * 4);
+                pos[nt][e] = __shfl_sync(0xFFFFFFFFu, pr, (2 * c + e) * 4);
+            }
+#pragma unroll
+            for (int k = 0; k < kChunks; ++k)
+#pragma unroll
+                for (int s = 0; s < 4; ++s) {
+                    qb[nt][k * 4 + s][0] = raw[k][2 * s];
+                    qb[nt][k * 4 + s][1] = raw[k][2 * s + 1];
+                }
+        }
+        // a tile inside [see0, see1] is visible to every row of the item
+        const int see1 = cur.L - cur.n + work.token(cur, 0).x;
+        const int see0 = !LIST && p.a.window ? cur.L - cur.n + work.token(cur, rows - 1).x - p.a.window + 1 : 0;
 
-        float o[MT][kNt][4];
-        float m[MT][2], l[MT][2], M[MT][2];
+        float o[NT][kCh / 2][4];
+        float m[NT][2], l[NT][2], M[NT][2];
 #pragma unroll
-        for (int mt = 0; mt < MT; ++mt) {
+        for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
-            for (int i = 0; i < kNt; ++i)
+            for (int i = 0; i < kCh / 2; ++i)
 #pragma unroll
-                for (int e = 0; e < 4; ++e) o[mt][i][e] = 0.0f;
+                for (int e = 0; e < 4; ++e) o[nt][i][e] = 0.0f;
 #pragma unroll
-            for (int half = 0; half < 2; ++half) m[mt][half] = M[mt][half] = kNone, l[mt][half] = 0.0f;
+            for (int e = 0; e < 2; ++e) m[nt][e] = M[nt][e] = kNone, l[nt][e] = 0.0f;
         }
 
 #pragma unroll 1
         for (int i = 0; i < todo; ++i) {
             // refill the slot that was read last, then look at the next tile's scales
-            {
-                const int fill = slot == 0 ? kStages - 1 : slot - 1;
-                issue(fill);
-                lookup();
-                peek();
-            }
-            const int unit = here.x, t0 = here.y;
-            const float ks_now = ks, vs_now = vs;
+            issue(slot == 0 ? kStages - 1 : slot - 1);
+            lookup();
+            peek();
+            const int4 tile = here;
+            const float ks_now[2] = {ks[0], ks[1]}, vs_now[2] = {vs[0], vs[1]};
             const int now = slot;
             slot = slot + 1 == kStages ? 0 : slot + 1;
             __syncwarp();
             here = slots[slot];
-            if (here.x >= 0) {
-                ks = __ldg(p.c.k_scale + here.x);
-                vs = __ldg(p.c.v_scale + here.x);
-            }
-            if (unit < 0) continue;
+            scales();
+            if (tile.x < 0 && tile.z < 0) continue;
             if (alive) {
                 alive = tc::mbar_wait(bars + now, (phase >> now) & 1u, p.wait_limit);
                 if (!alive && lane == 0) flag(p.a.status, kStatusTimeout);
             }
             alive = __all_sync(0xFFFFFFFFu, alive);
             if (!alive) {
-                issued |= 1u << now;
+                late |= 1u << now;
                 continue;
             }
             phase ^= 1u << now;
-            const uint8_t* kt = ring + now * 2 * S::kRows;
-            const uint8_t* vt = kt + S::kRows;
-
-            // ---- S = Q K^T, two n tiles of eight positions
-            float s[MT][2][4];
+            uint8_t* kt = ring + now * 2 * S::kRows;
+            uint8_t* vt = kt + S::kRows;
+            const bool inside = tile.x >= 0 && tile.z >= 0 && tile.y >= see0 && tile.w + kGroup - 1 <= see1;
+            if (!inside) {
+                // what lies behind the sequence's end, or was not copied, may be any code: NaN times a
+                // weight of 0 is NaN, so those value rows are cleared
+                bool cleared = false;
 #pragma unroll
-            for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-                for (int nt = 0; nt < 2; ++nt)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) s[mt][nt][e] = 0.0f;
-#pragma unroll
-            for (int nt = 0; nt < 2; ++nt)
-#pragma unroll
-                for (int k = 0; k < kChunks; ++k) {
-                    const uint32_t row = nt * 8 + r, chunk = c * kChunks + k;
-                    const uint4 w = *reinterpret_cast<const uint4*>(
-                        kt + (D == 128 ? tc::sw128_offset(row, chunk) : tc::sw64_offset(row, chunk)));
-                    const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-                    for (int q4 = 0; q4 < 4; ++q4) {
-                        uint32_t even, odd;
-                        e4m3x4_to_half(ww[q4], even, odd);
-#pragma unroll
-                        for (int mt = 0; mt < MT; ++mt) mma_16816(s[mt][nt], qa[mt][k * 4 + q4], even, odd);
+                for (int g = 0; g < 2; ++g)
+                    for (int x = lane; x < kGroup * (D / 16); x += 32) {
+                        const int row = x / (D / 16);
+                        if ((g ? tile.z : tile.x) < 0 || (g ? tile.w : tile.y) + row >= cur.L) {
+                            *reinterpret_cast<uint4*>(vt + g * kGroup * D + x * 16) = make_uint4(0, 0, 0, 0);
+                            cleared = true;
+                        }
                     }
-                }
+                if (cleared) tc::fence_proxy_async_smem();   // before a later copy into this slot
+                __syncwarp();
+            }
 
-            // ---- base-2 logits, masked; a vote tells whether a running maximum moves at all.  m: maximum of the logits (for l), M: of logit + log2(value scale) (for the output)
-            const float ev = (float)((int)(__float_as_uint(vs_now) >> 23) - 127);
+            // ---- S^T = K Q^T: group g, positions r and r + 8 of it, query rows 2c and 2c + 1 of every tile
+            float s[2][NT][4];
+#pragma unroll
+            for (int g = 0; g < 2; ++g)
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) s[g][nt][e] = 0.0f;
+#pragma unroll
+            for (int k = 0; k < kChunks; ++k) {
+                uint32_t w[2][2][4];
+#pragma unroll
+                for (int g = 0; g < 2; ++g)
+#pragma unroll
+                    for (int half = 0; half < 2; ++half) {
+                        const uint32_t row = g * kGroup + half * 8 + r, chunk = c * kChunks + k;
+                        const uint4 x = *reinterpret_cast<const uint4*>(
+                            kt + (D == 128 ? tc::sw128_offset(row, chunk) : tc::sw64_offset(row, chunk)));
+                        w[g][half][0] = x.x, w[g][half][1] = x.y, w[g][half][2] = x.z, w[g][half][3] = x.w;
+                    }
+#pragma unroll
+                for (int q4 = 0; q4 < 4; ++q4)
+#pragma unroll
+                    for (int g = 0; g < 2; ++g) {
+                        const uint32_t a[4] = {half2_lo(w[g][0][q4]), half2_lo(w[g][1][q4]), half2_hi(w[g][0][q4]),
+                                               half2_hi(w[g][1][q4])};
+#pragma unroll
+                        for (int nt = 0; nt < NT; ++nt)
+                            mma_16816(s[g][nt], a, qb[nt][k * 4 + q4][0], qb[nt][k * 4 + q4][1]);
+                    }
+            }
+
+            // ---- base-2 logits; a vote tells whether a running maximum moves at all.  m: maximum of the
+            // logits (for l), M: of logit + log2(value scale) (for the output)
+            float ev[2];
             bool over = false;
 #pragma unroll
-            for (int mt = 0; mt < MT; ++mt)
+            for (int g = 0; g < 2; ++g) {
+                ev[g] = (float)((int)(__float_as_uint(vs_now[g]) >> 23) - 127);
 #pragma unroll
-                for (int half = 0; half < 2; ++half) {
-                    const float f = zs[mt][half] * ks_now;
-                    const int pr = pos[mt][half];
-                    const int first = !LIST && p.a.window ? pr - p.a.window + 1 : 0;
+                for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                    for (int nt = 0; nt < 2; ++nt)
+                    for (int e = 0; e < 2; ++e) {
+                        const float f = zs[nt][e] * ks_now[g];
+                        s[g][nt][e] *= f;
+                        s[g][nt][2 + e] *= f;
+                    }
+            }
+            if (!inside) {
 #pragma unroll
-                        for (int e = 0; e < 2; ++e) {
-                            const int t = t0 + nt * 8 + 2 * c + e;
-                            float z = s[mt][nt][half * 2 + e] * f;
-                            z = t <= pr && t >= first ? z : -INFINITY;
-                            s[mt][nt][half * 2 + e] = z;
-                            over |= z > m[mt][half] || z + ev > M[mt][half];
+                for (int g = 0; g < 2; ++g) {
+                    const bool there = (g ? tile.z : tile.x) >= 0;
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            const int t = (g ? tile.w : tile.y) + r + (e >> 1) * 8, pr = pos[nt][e & 1];
+                            const bool in = there && t <= pr && (LIST || !p.a.window || t > pr - p.a.window);
+                            s[g][nt][e] = in ? s[g][nt][e] : -INFINITY;
                         }
+                }
+            }
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const float z0 = fmaxf(s[0][nt][e], s[0][nt][2 + e]), z1 = fmaxf(s[1][nt][e], s[1][nt][2 + e]);
+                    over |= fmaxf(z0, z1) > m[nt][e] || fmaxf(z0 + ev[0], z1 + ev[1]) > M[nt][e];
                 }
             if (__any_sync(0xFFFFFFFFu, over)) {
 #pragma unroll
-                for (int mt = 0; mt < MT; ++mt)
+                for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                    for (int half = 0; half < 2; ++half) {
-                        float z = fmaxf(fmaxf(s[mt][0][half * 2], s[mt][0][half * 2 + 1]),
-                                        fmaxf(s[mt][1][half * 2], s[mt][1][half * 2 + 1]));
-                        z = fmaxf(z, __shfl_xor_sync(0xFFFFFFFFu, z, 1));
-                        z = fmaxf(z, __shfl_xor_sync(0xFFFFFFFFu, z, 2));
-                        const float m1 = fmaxf(m[mt][half], z), M1 = fmaxf(M[mt][half], z + ev);
-                        l[mt][half] *= ex2(m[mt][half] - m1);
-                        const float fo = ex2(M[mt][half] - M1);
-                        m[mt][half] = m1;
-                        M[mt][half] = M1;
+                    for (int e = 0; e < 2; ++e) {
+                        const float z0 = fmaxf(s[0][nt][e], s[0][nt][2 + e]), z1 = fmaxf(s[1][nt][e], s[1][nt][2 + e]);
+                        float z = fmaxf(z0, z1), Z = fmaxf(z0 + ev[0], z1 + ev[1]);
 #pragma unroll
-                        for (int i2 = 0; i2 < kNt; ++i2) {
-                            o[mt][i2][half * 2] *= fo;
-                            o[mt][i2][half * 2 + 1] *= fo;
+                        for (int x = 4; x < 32; x <<= 1) {
+                            z = fmaxf(z, __shfl_xor_sync(0xFFFFFFFFu, z, x));
+                            Z = fmaxf(Z, __shfl_xor_sync(0xFFFFFFFFu, Z, x));
+                        }
+                        z = fmaxf(m[nt][e], z);
+                        Z = fmaxf(M[nt][e], Z);
+                        l[nt][e] *= ex2(m[nt][e] - z);
+                        const float f = ex2(M[nt][e] - Z);
+                        m[nt][e] = z;
+                        M[nt][e] = Z;
+#pragma unroll
+                        for (int i2 = 0; i2 < kCh / 2; ++i2) {
+                            o[nt][i2][e] *= f;
+                            o[nt][i2][2 + e] *= f;
                         }
                     }
             }
-            uint32_t pa[MT][4];
+            uint32_t pb[2][NT][2];
 #pragma unroll
-            for (int mt = 0; mt < MT; ++mt)
+            for (int g = 0; g < 2; ++g)
 #pragma unroll
-                for (int half = 0; half < 2; ++half)
+                for (int nt = 0; nt < NT; ++nt) {
+                    const float d0 = ev[g] - M[nt][0] + kHeadroom, d1 = ev[g] - M[nt][1] + kHeadroom;
 #pragma unroll
-                    for (int nt = 0; nt < 2; ++nt) {
-                        const float z0 = s[mt][nt][half * 2], z1 = s[mt][nt][half * 2 + 1];
-                        l[mt][half] += ex2(z0 - m[mt][half]) + ex2(z1 - m[mt][half]);
+                    for (int half = 0; half < 2; ++half) {
+                        const float z0 = s[g][nt][half * 2], z1 = s[g][nt][half * 2 + 1];
+                        l[nt][0] += ex2(z0 - m[nt][0]);
+                        l[nt][1] += ex2(z1 - m[nt][1]);
                         // fp16 keeps 11 bits of a weight: no fewer than the output's type keeps
-                        const float d = ev - M[mt][half] + kHeadroom;
-                        const __half2 h = __floats2half2_rn(ex2(z0 + d), ex2(z1 + d));
-                        memcpy(&pa[mt][nt * 2 + half], &h, 4);
+                        const __half2 h = __floats2half2_rn(ex2(z0 + d0), ex2(z1 + d1));
+                        uint32_t x;
+                        memcpy(&x, &h, 4);
+                        pb[g][nt][half] = transpose8x8(x);
                     }
-
-            // ---- O += P V: value rows 2c, 2c+1, 8+2c, 9+2c, this lane's D / 8 channels
-            uint32_t vw[4][kNt / 4];
-#pragma unroll
-            for (int i2 = 0; i2 < 4; ++i2) {
-                const uint32_t row = 2 * c + (i2 & 1) + (i2 >> 1) * 8;
-                if (D == 128) {
-                    const uint4 w = *reinterpret_cast<const uint4*>(vt + tc::sw128_offset(row, r));
-                    vw[i2][0] = w.x, vw[i2][1] = w.y, vw[i2][kNt / 4 - 2] = w.z, vw[i2][kNt / 4 - 1] = w.w;
-                } else {
-                    const uint2 w = *reinterpret_cast<const uint2*>(vt + tc::sw64_offset(row, r >> 1) + (r & 1) * 8);
-                    vw[i2][0] = w.x, vw[i2][1] = w.y;
                 }
-            }
+
+            // ---- O^T += V^T P^T: positions 2c, 2c+1, 8+2c, 9+2c of a group, this lane's D / 8 channels
 #pragma unroll
-            for (int i2 = 0; i2 < kNt / 4; ++i2) {
-                const uint32_t a0 = vw[0][i2], a1 = vw[1][i2], b0 = vw[2][i2], b1 = vw[3][i2];
-                const uint32_t f0 = e4m3_pair<0>(a0, a1), g0 = e4m3_pair<0>(b0, b1);
-                const uint32_t f1 = e4m3_pair<1>(a0, a1), g1 = e4m3_pair<1>(b0, b1);
-                const uint32_t f2 = e4m3_pair<2>(a0, a1), g2 = e4m3_pair<2>(b0, b1);
-                const uint32_t f3 = e4m3_pair<3>(a0, a1), g3 = e4m3_pair<3>(b0, b1);
+            for (int g = 0; g < 2; ++g) {
+                uint32_t w[4][kCh / 4];
 #pragma unroll
-                for (int mt = 0; mt < MT; ++mt) {
-                    mma_16816(o[mt][i2 * 4 + 0], pa[mt], f0, g0);
-                    mma_16816(o[mt][i2 * 4 + 1], pa[mt], f1, g1);
-                    mma_16816(o[mt][i2 * 4 + 2], pa[mt], f2, g2);
-                    mma_16816(o[mt][i2 * 4 + 3], pa[mt], f3, g3);
+                for (int x = 0; x < 4; ++x) {
+                    const uint32_t row = g * kGroup + 2 * c + (x & 1) + (x >> 1) * 8;
+                    if (D == 128) {
+                        const uint4 y = *reinterpret_cast<const uint4*>(vt + tc::sw128_offset(row, r));
+                        w[x][0] = y.x, w[x][1] = y.y, w[x][kCh / 4 - 2] = y.z, w[x][kCh / 4 - 1] = y.w;
+                    } else {
+                        const uint2 y = *reinterpret_cast<const uint2*>(vt + tc::sw64_offset(row, r >> 1) + (r & 1) * 8);
+                        w[x][0] = y.x, w[x][1] = y.y;
+                    }
+                }
+#pragma unroll
+                for (int i2 = 0; i2 < kCh / 4; ++i2) {
+                    // one channel of two positions side by side
+                    const uint32_t x01 = __byte_perm(w[0][i2], w[1][i2], 0x5140), x23 = __byte_perm(w[0][i2], w[1][i2], 0x7362);
+                    const uint32_t y01 = __byte_perm(w[2][i2], w[3][i2], 0x5140), y23 = __byte_perm(w[2][i2], w[3][i2], 0x7362);
+                    const uint32_t a01[4] = {half2_lo(x01), half2_hi(x01), half2_lo(y01), half2_hi(y01)};
+                    const uint32_t a23[4] = {half2_lo(x23), half2_hi(x23), half2_lo(y23), half2_hi(y23)};
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt) {
+                        mma_16816(o[nt][i2 * 2], a01, pb[g][nt][0], pb[g][nt][1]);
+                        mma_16816(o[nt][i2 * 2 + 1], a23, pb[g][nt][0], pb[g][nt][1]);
+                    }
                 }
             }
             __syncwarp();
@@ -574,90 +662,87 @@ __global__ void __launch_bounds__(kThreads, MT == 1 ? 3 : 2) k_kv8_attn(const __
         float* stats = reinterpret_cast<float*>(smem + S::stats);
         float* buf = reinterpret_cast<float*>(smem + S::merge);
 #pragma unroll
-        for (int mt = 0; mt < MT; ++mt)
+        for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-            for (int half = 0; half < 2; ++half) {
-                l[mt][half] += __shfl_xor_sync(0xFFFFFFFFu, l[mt][half], 1);
-                l[mt][half] += __shfl_xor_sync(0xFFFFFFFFu, l[mt][half], 2);
-                if (c == 0) {
-                    float* s3 = stats + (warp * 16 * MT + mt * 16 + half * 8 + r) * 3;
-                    s3[0] = m[mt][half];
-                    s3[1] = l[mt][half];
-                    s3[2] = M[mt][half];
+            for (int e = 0; e < 2; ++e) {
+#pragma unroll
+                for (int x = 4; x < 32; x <<= 1) l[nt][e] += __shfl_xor_sync(0xFFFFFFFFu, l[nt][e], x);
+                if (r == 0) {
+                    float* s3 = stats + (warp * 8 * NT + nt * 8 + 2 * c + e) * 3;
+                    s3[0] = m[nt][e];
+                    s3[1] = l[nt][e];
+                    s3[2] = M[nt][e];
                 }
             }
         __syncthreads();
-        float mx[MT][2], lx[MT][2], Mx[MT][2];
 #pragma unroll
-        for (int mt = 0; mt < MT; ++mt)
+        for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-            for (int half = 0; half < 2; ++half) {
-                const float* s3 = stats + (mt * 16 + half * 8 + r) * 3;
+            for (int e = 0; e < 2; ++e) {
+                const float* s3 = stats + (nt * 8 + 2 * c + e) * 3;
                 float a = kNone, B = kNone, sum = 0.0f;
 #pragma unroll
                 for (int w = 0; w < kWarps; ++w) {
-                    a = fmaxf(a, s3[w * 48 * MT]);
-                    B = fmaxf(B, s3[w * 48 * MT + 2]);
+                    a = fmaxf(a, s3[w * 24 * NT]);
+                    B = fmaxf(B, s3[w * 24 * NT + 2]);
                 }
 #pragma unroll
-                for (int w = 0; w < kWarps; ++w) sum += s3[w * 48 * MT + 1] * ex2(s3[w * 48 * MT] - a);
-                mx[mt][half] = a;
-                lx[mt][half] = sum;
-                Mx[mt][half] = B;
-                const float f = ex2(M[mt][half] - B);
+                for (int w = 0; w < kWarps; ++w) sum += s3[w * 24 * NT + 1] * ex2(s3[w * 24 * NT] - a);
+                const float f = ex2(M[nt][e] - B);
+                m[nt][e] = a;
+                l[nt][e] = sum;
+                M[nt][e] = B;
 #pragma unroll
-                for (int i2 = 0; i2 < kNt; ++i2) {
-                    o[mt][i2][half * 2] *= f;
-                    o[mt][i2][half * 2 + 1] *= f;
+                for (int i2 = 0; i2 < kCh / 2; ++i2) {
+                    o[nt][i2][e] *= f;
+                    o[nt][i2][2 + e] *= f;
                 }
             }
-        // eight rows (r, half `half` of a row tile) a pass: warp w sums register e = w & 1 of half the n
-        // tiles, that is kNt / 2 adjacent channels of lane column 2c + e
+        // a pass: eight rows, eight of each lane's channels; warp w sums four of them for row 2c + (w & 1)
         const bool whole = from_start && to_end;
         float* part = p.a.part + ((int64_t)blockIdx.x * 2 + (from_start ? 1 : 0)) * Part<D>::kFloats;
+        const int e = warp & 1, hh = warp >> 1;
 #pragma unroll
-        for (int mt = 0; mt < MT; ++mt)
+        for (int nt = 0; nt < NT; ++nt) {
+            if (nt * 8 >= rows) continue;
 #pragma unroll
-            for (int half = 0; half < 2; ++half) {
-                if (mt * 16 + half * 8 >= rows) continue;
+            for (int ps = 0; ps < kCh / 8; ++ps) {
+#pragma unroll
+                for (int x = 0; x < 16; ++x) buf[(warp * 16 + x) * 32 + lane] = o[nt][ps * 4 + x / 4][x & 3];
                 __syncthreads();
+                const int row = nt * 8 + 2 * c + e;
+                if (row < rows && alive) {
+                    float y[4];
 #pragma unroll
-                for (int e = 0; e < 2; ++e)
+                    for (int x = 0; x < 4; ++x) {
+                        const int reg = (hh * 2 + x / 2) * 4 + (x & 1) * 2 + e;
+                        y[x] = 0.0f;
 #pragma unroll
-                    for (int i2 = 0; i2 < kNt; ++i2)
-                        buf[((warp * 2 + e) * kNt + i2) * 32 + lane] = o[mt][i2][half * 2 + e];
-                __syncthreads();
-                const int row = mt * 16 + half * 8 + r, e = warp & 1, n0 = (warp >> 1) * (kNt / 2);
-                const int ch = (2 * c + e) * kNt + n0;
-                if (row >= rows || !alive) continue;
-                float x[kNt / 2];
-#pragma unroll
-                for (int i2 = 0; i2 < kNt / 2; ++i2) {
-                    x[i2] = 0.0f;
-#pragma unroll
-                    for (int w = 0; w < kWarps; ++w) x[i2] += buf[((w * 2 + e) * kNt + n0 + i2) * 32 + lane];
-                }
-                const float lr = lx[mt][half], mr = mx[mt][half], Mr = Mx[mt][half];
-                if (whole) {
-                    const int2 jg = work.token(cur, row);
-                    const int64_t at = ((int64_t)cur.b * T + jg.x) * H + cur.h * G + jg.y;
-                    const float f = lr == 0.0f ? 0.0f : ex2(Mr - mr) / lr;
-                    store_out<kNt / 2>(p.a.out, p.a.q.is_bf16, at * D + ch, x, f);
-                    if (p.a.lse && c == 0 && warp == 0)
-                        p.a.lse[at] = lr == 0.0f ? -INFINITY : (mr + log2f(lr)) * 0.6931471805599453f;
-                } else {
-                    float4* dst = reinterpret_cast<float4*>(part + row * D + ch);
-#pragma unroll
-                    for (int i2 = 0; i2 < kNt / 2; i2 += 4)
-                        dst[i2 / 4] = make_float4(x[i2], x[i2 + 1], x[i2 + 2], x[i2 + 3]);
-                    if (c == 0 && warp == 0) {
-                        float* s3 = part + Part<D>::kStats + row * 3;
-                        s3[0] = mr;
-                        s3[1] = lr;
-                        s3[2] = Mr;
+                        for (int w = 0; w < kWarps; ++w) y[x] += buf[(w * 16 + reg) * 32 + lane];
+                    }
+                    const int ch = r * kCh + ps * 8 + hh * 4;
+                    const float lr = e ? l[nt][1] : l[nt][0], mr = e ? m[nt][1] : m[nt][0],
+                                Mr = e ? M[nt][1] : M[nt][0];
+                    const bool first = ps == 0 && r == 0 && hh == 0;
+                    if (whole) {
+                        const int2 jg = work.token(cur, row);
+                        const int64_t at = ((int64_t)cur.b * T + jg.x) * H + cur.h * G + jg.y;
+                        store_out(p.a.out, p.a.q.is_bf16, at * D + ch, y,
+                                  lr == 0.0f ? 0.0f : ex2(Mr - mr - kHeadroom) / lr);
+                        if (p.a.lse && first) p.a.lse[at] = lr == 0.0f ? -INFINITY : (mr + log2f(lr)) * 0.6931471805599453f;
+                    } else {
+                        *reinterpret_cast<float4*>(part + row * D + ch) = make_float4(y[0], y[1], y[2], y[3]);
+                        if (first) {
+                            float* s3 = part + Part<D>::kStats + row * 3;
+                            s3[0] = mr;
+                            s3[1] = lr;
+                            s3[2] = Mr;
+                        }
                     }
                 }
+                __syncthreads();
             }
+        }
         if (from_start && !to_end && tid == 0) {  // the pieces up to the one with the item's last step
             const int64_t last_u = u + item_left - 1;
             const int64_t last = ((last_u + 1) * share + total - 1) / total - 1;
@@ -670,19 +755,16 @@ __global__ void __launch_bounds__(kThreads, MT == 1 ? 3 : 2) k_kv8_attn(const __
         u += todo;
         cur.step += todo - 1;
         if (++cur.step >= cur.steps) work.next_item(cur);
-        __syncthreads();
     }
     // copies that were given up on still land in this CTA's memory
-    if (!alive) {
-        for (int i = 0; i < kStages; ++i)
-            if ((issued >> i) & 1u) tc::mbar_wait(bars + i, (phase >> i) & 1u);
-    }
+    for (int i = 0; i < kStages; ++i)
+        if ((late >> i) & 1u) tc::mbar_wait(bars + i, (phase >> i) & 1u);
 }
 
 // The items that the line's cuts went through: CTA x merges the item that
 // starts in piece x and goes on behind it, four rows per blockIdx.y, the parts
 // of a row in four shares, each in the order of the pieces.
-template <int D, int MT, bool LIST>
+template <int D, int NT, bool LIST>
 __global__ void __launch_bounds__(4 * D) k_kv8_combine(const __grid_constant__ Params p) {
     constexpr int kLanes = D / 4, kShares = 4, kRows = 4;
     __shared__ float4 acc[kRows][kShares][kLanes];
@@ -740,34 +822,44 @@ __global__ void __launch_bounds__(4 * D) k_kv8_combine(const __grid_constant__ P
         y[2] += v.z;
         y[3] += v.w;
     }
-    const Work<MT, LIST> work(p);
+    const Work<NT, LIST> work(p);
     Cursor k;
     k.rt = desc[2];
     const int2 jg = work.token(k, row);
     const int64_t at = ((int64_t)desc[0] * p.a.q.T + jg.x) * p.a.q.H + desc[1] * p.G + jg.y;
-    store_out<4>(p.a.out, p.a.q.is_bf16, at * D + q4 * 4, y, l == 0.0f ? 0.0f : ex2(M - m) / l);
+    store_out(p.a.out, p.a.q.is_bf16, at * D + q4 * 4, y, l == 0.0f ? 0.0f : ex2(M - m - kHeadroom) / l);
     if (p.a.lse && q4 == 0) p.a.lse[at] = l == 0.0f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
 }
 
-template <int D, int MT, bool LIST>
+template <int D, int NT, bool LIST>
 cudaError_t launch(Params& p, cudaStream_t st) {
-    using S = Smem<D, MT>;
-    static_assert(S::bytes * (MT == 1 ? 3 : 2) <= 227 * 1024, "CTAs per SM");
+    using S = Smem<D, NT>;
+    constexpr int kPerSm = NT <= 2 ? 3 : 2;
+    static_assert(S::bytes * kPerSm + kPerSm * 1024 <= 228 * 1024, "CTAs per SM");
     int dev = 0, sms = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
     if (e != cudaSuccess) return e;
-    p.ctas = sms * (MT == 1 ? 3 : 2);
-    if (p.ctas > kMaxCtas) p.ctas = kMaxCtas;
-    p.gt = (p.G + 16 * MT - 1) / (16 * MT);
+    p.ctas = sms * kPerSm < kMaxCtas ? sms * kPerSm : kMaxCtas;
+    p.gt = (p.G + 8 * NT - 1) / (8 * NT);
     CUtensorMap kmap, vmap;
-    if (!kv8_row_map(&kmap, p.c, p.c.k, kTile) || !kv8_row_map(&vmap, p.c, p.c.v, kTile)) return cudaErrorNotSupported;
-    e = cudaFuncSetAttribute(k_kv8_attn<D, MT, LIST>, cudaFuncAttributeMaxDynamicSharedMemorySize, S::bytes);
+    const int box = p.c.bs() < kTile ? p.c.bs() : kTile;
+    if (!kv8_row_map(&kmap, p.c, p.c.k, box) || !kv8_row_map(&vmap, p.c, p.c.v, box)) return cudaErrorNotSupported;
+    e = cudaFuncSetAttribute(k_kv8_attn<D, NT, LIST>, cudaFuncAttributeMaxDynamicSharedMemorySize, S::bytes);
     if (e != cudaSuccess) return e;
-    e = launch_pdl(k_kv8_attn<D, MT, LIST>, p.ctas, kThreads, S::bytes, st, p, kmap, vmap);
+    e = launch_pdl(k_kv8_attn<D, NT, LIST>, p.ctas, kThreads, S::bytes, st, p, kmap, vmap);
     if (e != cudaSuccess) return e;
-    const int most = LIST ? (p.G < 16 * MT ? p.G : 16 * MT) : ((int64_t)p.a.q.T * p.G < 16 * MT ? p.a.q.T * p.G : 16 * MT);
-    return launch_pdl(k_kv8_combine<D, MT, LIST>, dim3(p.ctas, (most + 3) / 4), 4 * D, 0, st, p);
+    const int64_t rows = LIST ? p.G : (int64_t)p.a.q.T * p.G;
+    const int most = rows < 8 * NT ? (int)rows : 8 * NT;
+    return launch_pdl(k_kv8_combine<D, NT, LIST>, dim3(p.ctas, (most + 3) / 4), 4 * D, 0, st, p);
+}
+
+template <int D>
+cudaError_t launch_d(Params& p, cudaStream_t st) {
+    if (p.a.block_idx) return p.G <= 8 ? launch<D, 1, true>(p, st) : launch<D, 2, true>(p, st);
+    const int64_t rows = (int64_t)p.a.q.T * p.G;
+    if (rows <= 8) return launch<D, 1, false>(p, st);
+    return rows <= 16 ? launch<D, 2, false>(p, st) : launch<D, 4, false>(p, st);
 }
 
 }  // namespace
@@ -810,9 +902,7 @@ cudaError_t launch_kv8_attn(const DevKv8& c, const Kv8Attn& a, cudaStream_t st) 
     p.a = a;
     p.G = a.q.H / c.heads;
     p.wait_limit = wait_limit();
-    if (a.block_idx) return c.dim == 64 ? launch<64, 1, true>(p, st) : launch<128, 1, true>(p, st);
-    if ((int64_t)a.q.T * p.G <= 16) return c.dim == 64 ? launch<64, 1, false>(p, st) : launch<128, 1, false>(p, st);
-    return c.dim == 64 ? launch<64, 2, false>(p, st) : launch<128, 2, false>(p, st);
+    return c.dim == 64 ? launch_d<64>(p, st) : launch_d<128>(p, st);
 }
 
 }  // namespace csa2
