@@ -87,23 +87,16 @@ __device__ __forceinline__ float exp2_int(int e) {  // -126 <= e <= 127
     return __uint_as_float((uint32_t)(e + 127) << 23);
 }
 
-// Four E4M3 bytes -> two half2 holding value * 2^-8: the code's seven exponent
-// and mantissa bits are placed at the top of fp16's (4 exponent bits under a
-// bias of 15 instead of 7: a factor of 2^-8, subnormals included).  `even` is
-// bytes 0 and 2, `odd` bytes 1 and 3.  The NaN codes 0x7F / 0xFF, which the
-// append never writes, read as +-480.
-__device__ __forceinline__ void e4m3x4_to_half(uint32_t w, uint32_t& even, uint32_t& odd) {
-    const uint32_t s = w << 8;
-    even = ((w << 7) & 0x3F803F80u) | (s & 0x80008000u);
-    odd = ((w >> 1) & 0x3F803F80u) | (w & 0x80008000u);
+// Two E4M3 codes in the low (high) half of w -> half2; exact.
+__device__ __forceinline__ uint32_t half2_lo(uint32_t w) {
+    uint32_t r;
+    asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, l;\n\t}" : "=r"(r) : "r"(w));
+    return r;
 }
-
-// Byte `i` of a and of b -> half2 (a's low) holding value * 2^-8.
-template <int I>
-__device__ __forceinline__ uint32_t e4m3_pair(uint32_t a, uint32_t b) {
-    constexpr uint32_t sel = (uint32_t)(I << 4) | (uint32_t)((I + 4) << 12);
-    const uint32_t x = __byte_perm(a, b, sel);
-    return ((x >> 1) & 0x3F803F80u) | (x & 0x80008000u);
+__device__ __forceinline__ uint32_t half2_hi(uint32_t w) {
+    uint32_t r;
+    asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, h;\n\t}" : "=r"(r) : "r"(w));
+    return r;
 }
 
 __device__ __forceinline__ void mma_16816(float* c, const uint32_t* a, uint32_t b0, uint32_t b1) {

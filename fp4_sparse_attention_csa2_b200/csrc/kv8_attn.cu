@@ -221,18 +221,6 @@ __device__ __forceinline__ void store_out(void* out, int is_bf16, int64_t at, co
     *reinterpret_cast<uint2*>(dst) = make_uint2(w[0], w[1]);
 }
 
-// Two E4M3 codes in the low (high) half of w -> half2; exact.
-__device__ __forceinline__ uint32_t half2_lo(uint32_t w) {
-    uint32_t r;
-    asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, l;\n\t}" : "=r"(r) : "r"(w));
-    return r;
-}
-__device__ __forceinline__ uint32_t half2_hi(uint32_t w) {
-    uint32_t r;
-    asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, h;\n\t}" : "=r"(r) : "r"(w));
-    return r;
-}
-
 __device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
     uint32_t r;
     asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
