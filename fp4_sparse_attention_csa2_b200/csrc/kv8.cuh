@@ -120,8 +120,8 @@ cudaError_t launch_kv8_read(const DevKv8& c, const int32_t* start, const int32_t
                             void* v_out, int dtype, uint32_t* status, cudaStream_t st);
 
 // Attention over the cache (block_idx == nullptr: every visible position of
-// the window; else the listed blocks).  part: kv8_attn_parts() slots of
-// kv8_part_floats(dim) floats.
+// the window; else the listed blocks).  part: the partials of cut items, so
+// many floats as the kernel's *_part_floats says.
 struct Kv8Attn {
     Kv8Query q;
     const int32_t* block_idx;
@@ -136,9 +136,14 @@ struct Kv8Attn {
 // boxes of box_rows rows, the rows swizzled by their own length (128 or 64 B).
 bool kv8_row_map(CUtensorMap_st* map, const DevKv8& c, void* codes, int box_rows);
 
-int kv8_attn_parts();
-size_t kv8_part_floats(int dim);
+// Query rows of a key head (tokens x query heads) up to which the dense
+// attention runs as the streaming kernel (kv8_attn.cu), beyond it as the
+// tensor-core kernel (kv8_prefill.cu).
+constexpr int64_t kKv8StreamRows = 32;
+size_t kv8_attn_part_floats(int dim);
+size_t kv8_prefill_part_floats(int dim);
 cudaError_t launch_kv8_attn(const DevKv8& c, const Kv8Attn& a, cudaStream_t st);
+cudaError_t launch_kv8_prefill(const DevKv8& c, const Kv8Attn& a, cudaStream_t st);
 
 cudaError_t launch_kv8_select(const DevKv8& c, const Kv8Query& q, int n_sel, int n_first, int n_recent,
                               int32_t* block_idx, float* scores, uint32_t* status, cudaStream_t st);

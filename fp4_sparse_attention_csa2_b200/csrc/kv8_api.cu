@@ -62,7 +62,9 @@ bool make_layout(const csa2_kv8_cache* c, int T, int H, int n_sel, Layout* L) {
     if ((int64_t)T * H >= kMaxRows || (int64_t)c->batch * T * c->n_kv_heads >= kMaxRows) return false;
     size_t off = 256;
     L->part = off;
-    off += (size_t)kv8_attn_parts() * kv8_part_floats(c->head_dim) * sizeof(float);
+    const bool wide = (int64_t)T * (H / c->n_kv_heads) > kKv8StreamRows;
+    const size_t stream = kv8_attn_part_floats(c->head_dim), prefill = kv8_prefill_part_floats(c->head_dim);
+    off += (wide && prefill > stream ? prefill : stream) * sizeof(float);
     off = (off + 255) / 256 * 256;
     L->scores = off;
     if (n_sel) off += (size_t)c->batch * T * c->n_kv_heads * c->max_blocks * sizeof(float);
@@ -107,7 +109,9 @@ csa2_status attention(const csa2_kv8_cache* c, const Kv8Query& q, const int32_t*
     a.lse = lse;
     a.part = at<float>(ws, L.part);
     a.status = at<uint32_t>(ws, 0);
-    return cuda_status(launch_kv8_attn(dev_kv8(c), a, static_cast<cudaStream_t>(stream)));
+    const bool wide = !block_idx && (int64_t)q.T * (q.H / c->n_kv_heads) > kKv8StreamRows;
+    const cudaStream_t st = static_cast<cudaStream_t>(stream);
+    return cuda_status(wide ? launch_kv8_prefill(dev_kv8(c), a, st) : launch_kv8_attn(dev_kv8(c), a, st));
 }
 
 }  // namespace

@@ -881,8 +881,9 @@ bool kv8_row_map(CUtensorMap_st* map, const DevKv8& c, void* codes, int box_rows
                CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-int kv8_attn_parts() { return 2 * kMaxCtas; }
-size_t kv8_part_floats(int dim) { return dim == 64 ? Part<64>::kFloats : Part<128>::kFloats; }
+size_t kv8_attn_part_floats(int dim) {
+    return (size_t)2 * kMaxCtas * (dim == 64 ? Part<64>::kFloats : Part<128>::kFloats);
+}
 
 cudaError_t launch_kv8_attn(const DevKv8& c, const Kv8Attn& a, cudaStream_t st) {
     Params p;

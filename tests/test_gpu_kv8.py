@@ -359,6 +359,76 @@ def test_attn_wait_that_runs_out():
     assert csa2.read_device_status(ws) == csa2.OK and torch.equal(out, want)
 
 
+# ---------------------------------------------------------------- many query rows (the tensor-core kernel)
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+@pytest.mark.parametrize("heads,G,D,bs,lens,T,window", [
+    (1, 8, 128, 64, [400], 100, 0),          # several row blocks, the last not full
+    (2, 4, 64, 16, [130, 257, 90], 70, 0),   # ragged, head_dim 64, blocks of 16
+    (3, 5, 128, 128, [300, 220], 60, 0),     # groups that do not divide a row block
+    (1, 33, 128, 32, [64, 40], 8, 0),
+    (2, 8, 128, 64, [1500], 40, 200), (1, 4, 64, 32, [700, 300], 130, 129), (2, 2, 128, 16, [515], 515, 0),
+    (1, 1, 128, 64, [33, 2000], 33, 0),
+])
+def test_attn_many_rows(heads, G, D, bs, lens, T, window, dtype):
+    T = min(T, min(lens))
+    dev, r = both_caches(len(lens), heads, D, bs, (max(lens) + bs - 1) // bs + 1)
+    fill(dev, r, lens)
+    attend(dev, r, lens, T, heads * G, window=window, dtype=DT[dtype])
+
+
+def test_attn_many_rows_padded_and_empty():
+    # padded batch; a sequence without rows, one shorter than its rows (the first rows see nothing), length 0
+    lens, n = [300, 500, 20, 0, 129], [60, 0, 50, 64, 1]
+    dev, r = both_caches(5, 2, 128, 64, 9)
+    fill(dev, r, lens)
+    for window in (0, 3):
+        attend(dev, r, lens, 64, 8, n=n, window=window)
+    attend(dev, r, lens, 64, 8, n=[0] * 5)
+
+
+@pytest.mark.parametrize("q_scale,spread", [(2.0 ** -60, 1.0), (1.0, 7.0), (6.0, 3.0)])
+def test_attn_many_rows_magnitudes(q_scale, spread):
+    lens = [777]
+    dev, r = both_caches(1, 2, 128, 64, 13)
+    fill(dev, r, lens, spread=spread)
+    k = dev.k_scale.clone()
+    dev.k_scale.copy_(torch.where(torch.isnan(k), k, torch.full_like(k, 2.0 ** -6)))
+    r.ks[:] = 2.0 ** -6
+    attend(dev, r, lens, 24, 8, q_scale=q_scale)
+
+
+def test_attn_many_rows_zero_values():
+    # a block of zero values has the least scale there is and still counts in the sum
+    lens, D = [256], 128
+    dev, r = both_caches(1, 1, D, 64, 5)
+    g = torch.Generator().manual_seed(3)
+    k, v = torch.randn(1, 256, 1, D, generator=g), torch.randn(1, 256, 1, D, generator=g)
+    v[:, :64] = 0
+    v[:, 128:192] = 0
+    csa2.kv8_append(dev, k.cuda(), v.cuda(), i32([0]))
+    r.append(0, 0, k[0].double().numpy(), v[0].double().numpy())
+    dev.seq_lens.fill_(256)
+    attend(dev, r, lens, 64, 4)
+    attend(dev, r, lens, 1, 4)
+
+
+def test_attn_many_rows_wait_that_runs_out():
+    lens = [900]
+    dev, r = both_caches(1, 2, 128, 64, 16)
+    fill(dev, r, lens)
+    q = torch.randn(1, 100, 8, 128, generator=torch.Generator().manual_seed(1)).bfloat16().cuda()
+    want, out, ws = torch.zeros_like(q), torch.zeros_like(q), workspace(dev, 100, 8)
+    csa2.kv8_attn(dev, q, want, ws)
+    csa2.debug_set_wait_limit(0)
+    try:
+        csa2.kv8_attn(dev, q, out, ws)
+    finally:
+        csa2.debug_set_wait_limit()
+    assert csa2.read_device_status(ws) == csa2.ERR_TIMEOUT
+    csa2.kv8_attn(dev, q, out, ws)
+    assert csa2.read_device_status(ws) == csa2.OK and torch.equal(out, want)
+
+
 def test_offsets_beyond_32_bits():
     # codes of more than 4 GiB a side: the sequence's blocks lie at the far end
     heads, D, bs, mb = 8, 128, 64, 5
