@@ -133,8 +133,9 @@ struct Kv8Attn {
     uint32_t* status;
 };
 // The codes as a 2-D byte tensor [blocks * heads * block_size][dim] for TMA
-// boxes of box_rows rows, the rows swizzled by their own length (128 or 64 B).
-bool kv8_row_map(CUtensorMap_st* map, const DevKv8& c, void* codes, int box_rows);
+// boxes of box_rows rows; `swizzled`: rows swizzled by their own length (128 or
+// 64 B) in shared memory, else dense.
+bool kv8_row_map(CUtensorMap_st* map, const DevKv8& c, void* codes, int box_rows, bool swizzled);
 
 // Query rows of a key head (tokens x query heads) up to which the dense
 // attention runs as the streaming kernel (kv8_attn.cu), beyond it as the

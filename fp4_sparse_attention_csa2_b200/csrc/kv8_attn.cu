@@ -832,7 +832,7 @@ cudaError_t launch(Params& p, cudaStream_t st) {
     p.gt = (p.G + 8 * NT - 1) / (8 * NT);
     CUtensorMap kmap, vmap;
     const int box = p.c.bs() < kTile ? p.c.bs() : kTile;
-    if (!kv8_row_map(&kmap, p.c, p.c.k, box) || !kv8_row_map(&vmap, p.c, p.c.v, box)) return cudaErrorNotSupported;
+    if (!kv8_row_map(&kmap, p.c, p.c.k, box, true) || !kv8_row_map(&vmap, p.c, p.c.v, box, true)) return cudaErrorNotSupported;
     e = cudaFuncSetAttribute(k_kv8_attn<D, NT, LIST>, cudaFuncAttributeMaxDynamicSharedMemorySize, S::bytes);
     if (e != cudaSuccess) return e;
     e = launch_pdl(k_kv8_attn<D, NT, LIST>, p.ctas, kThreads, S::bytes, st, p, kmap, vmap);
@@ -870,14 +870,15 @@ EncodeTiled encode_fn() {
 }
 }  // namespace
 
-bool kv8_row_map(CUtensorMap_st* map, const DevKv8& c, void* codes, int box_rows) {
+bool kv8_row_map(CUtensorMap_st* map, const DevKv8& c, void* codes, int box_rows, bool swizzled) {
     EncodeTiled enc = encode_fn();
     if (!enc) return false;
     const cuuint64_t gdim[2] = {(cuuint64_t)c.dim, ((cuuint64_t)c.n_blocks * c.heads) << c.bs_log2};
     const cuuint64_t gstride[1] = {(cuuint64_t)c.dim};
     const cuuint32_t box[2] = {(cuuint32_t)c.dim, (cuuint32_t)box_rows}, estride[2] = {1, 1};
     return enc(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, codes, gdim, gstride, box, estride,
-               CU_TENSOR_MAP_INTERLEAVE_NONE, c.dim == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+               CU_TENSOR_MAP_INTERLEAVE_NONE,
+               !swizzled ? CU_TENSOR_MAP_SWIZZLE_NONE : c.dim == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
                CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 

@@ -4,17 +4,20 @@
 // With the query rows of all tokens and the query heads of a key head as the
 // rows of a matrix (256 of them a CTA, two tiles of 128), both products are
 // GEMM-shaped and the tensor cores bound the kernel: 4 * 256 * 128 * D flop per
-// 128 positions.  One CTA per SM, four warpgroups:
-//   - two softmax warpgroups, one per row tile, a thread a row: read S from
-//     TMEM, keep the running maximum and sum, write the weights as fp16 over S
-//     (the second product takes them from TMEM), and rescale O on the rare step
-//     that moves the maximum by more than 2^4;
-//   - a converter warpgroup: the codes of the next 128 positions from global
-//     memory through registers to fp16 operand tiles (E4M3 values are exact in
-//     fp16; 1.5 % of a step's instructions), two stages deep;
-//   - one thread that issues every tcgen05.mma.  It alternates the row tiles
+// 128 positions.  One CTA per SM, six warpgroups:
+//   - four softmax warpgroups, two per row tile, a thread half a row (two
+//     halves a row keep a thread's 64 values in registers and halve the time
+//     from S to the weights, which is what the products wait for): read S from
+//     TMEM, agree on the running maximum, write the weights as fp16 over S (the
+//     second product takes them from TMEM), and rescale O on the rare step that
+//     moves the maximum by more than 2^4;
+//   - a converter warpgroup: the codes of the next 128 positions from where TMA
+//     put them to fp16 operand tiles (E4M3 values are exact in fp16), two
+//     stages deep;
+//   - one warp that issues every tcgen05.mma.  It alternates the row tiles
 //     (O0 += P0 V, S0 = Q0 K, O1 += P1 V, S1 = Q1 K), so one tile's products
-//     run while the other's softmax does.
+//     run while the other's softmax does;
+//   - one warp that looks up pages and issues the TMA loads.
 // Key scales multiply S per block; value scales enter the weights' exponent,
 // weight = 2^(z + log2(vs) - M), so the fp16 weights stay in range whatever the
 // blocks' scales are, and the sum takes them back out per block (exact powers
@@ -23,6 +26,7 @@
 // Work split as in kv8_attn.cu: the (row block, head, 128 positions) steps of
 // the batch form one line cut into equal pieces, cut items are merged by
 // k_kv8_prefill_combine.
+#include <cuda.h>
 #include <cuda_fp16.h>
 
 #include "kernels.h"
@@ -33,8 +37,9 @@ namespace csa2 {
 namespace {
 
 constexpr int kRows = 256, kTileRows = 128, kPos = 128;
-constexpr int kThreads = 512;
+constexpr int kThreads = 768, kConv = 128, kSoftmax = 512;   // all, converter's, softmax's
 constexpr int kMaxCtas = 148;
+constexpr int kMmaWarp = 20, kLoadWarp = 21;
 constexpr float kNone = -3.0e38f;
 constexpr float kHeadroom = 8.0f;   // weights are 2^(z - M + 8): full fp16 precision down to 2^-22
 constexpr float kLazy = 4.0f;       // and at most 2^12 before the maximum is moved
@@ -138,6 +143,32 @@ __device__ void line_find(const Line& w, const int64_t* sums, int64_t u, Cursor&
     k.step = k.steps ? (int)(u - (int64_t)k.h * k.steps) : 0;
 }
 
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    float r;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+    return r;
+}
+__device__ __forceinline__ uint64_t pack2(float x, float y) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(x), "f"(y));
+    return r;
+}
+__device__ __forceinline__ float2 unpack2(uint64_t v) {
+    float2 r;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+    return r;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+
 template <int D>
 struct Smem {
     static constexpr int kPanels = D / 64;                    // 64 channels (128 bytes of fp16) a panel
@@ -146,28 +177,33 @@ struct Smem {
     static constexpr int q = 0;                               // [row tile][panel]
     static constexpr int k = q + 2 * kTile;                   // [stage][panel]
     static constexpr int v = k + 2 * kTile;                   // [stage][panel]
-    static constexpr int sc = v + 2 * kTile;                  // [4][8] (key scale, log2 value scale)
-    static constexpr int bars = sc + 4 * 8 * 8;
-    static constexpr int misc = bars + 16 * 8;                // TMEM base, dead
-    static constexpr int sums = misc + 16;
-    static constexpr int bytes = sums + (kThreads + 1) * 8 + 1024;
+    static constexpr int codes = v + 2 * kTile;               // K, V as stored
+    static constexpr int sums = codes;                        // kThreads + 1 words, before the first load
+    static constexpr int sc = codes + 2 * kPos * D;           // [8][8] (key scale, log2 value scale)
+    static constexpr int lims = sc + 8 * 8 * 8;               // [8] positions of a tile before the sequence's end
+    static constexpr int xch = lims + 8 * 4;                  // [tile][half][128] floats: halves of a row agree
+    static constexpr int bars = xch + 4 * 128 * 4;
+    static constexpr int misc = bars + 24 * 8;                // TMEM base, dead, failed[2]
+    static constexpr int bytes = misc + 16;
 };
 
-enum Bar { kQ = 0, kKFull = 1, kKEmpty = 3, kVFull = 5, kVEmpty = 7, kS = 9, kP = 11, kO = 13, kDrain = 14 };  // pairs by stage or tile; kO one
+// Barriers, in pairs by stage or row tile (kLFull, kLEmpty: K, V).
+enum Bar { kQ = 0, kKFull = 1, kKEmpty = 3, kVFull = 5, kVEmpty = 7, kS = 9, kP = 11, kLFull = 13, kLEmpty = 15, kO = 17, kDrain = 18 };
 
 constexpr uint32_t kColO = 256;      // TMEM columns: S0, S1 (P over them), O0, O1
 
 template <int D>
-__global__ void __launch_bounds__(kThreads, 1) k_kv8_prefill(const __grid_constant__ Params p) {
+__global__ void __launch_bounds__(kThreads, 1) k_kv8_prefill(const __grid_constant__ Params p,
+                                                             const __grid_constant__ CUtensorMap kmap,
+                                                             const __grid_constant__ CUtensorMap vmap) {
     using S = Smem<D>;
-    extern __shared__ uint8_t smem_raw[];
-    uint8_t* smem = smem_raw + ((1024u - (tc::smem_u32(smem_raw) & 1023u)) & 1023u);
+    extern __shared__ __align__(1024) uint8_t smem[];   // no static shared memory: it starts on such a boundary
     uint64_t* bars = reinterpret_cast<uint64_t*>(smem + S::bars);
     volatile uint32_t* misc = reinterpret_cast<volatile uint32_t*>(smem + S::misc);
     int64_t* sums = reinterpret_cast<int64_t*>(smem + S::sums);
     float2* sc = reinterpret_cast<float2*>(smem + S::sc);
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, wg = tid >> 7, wt = tid & 127;
-    const int bs = p.c.bs(), G = p.G, T = p.a.q.T, H = p.a.q.H;
+    volatile int* lims = reinterpret_cast<volatile int*>(smem + S::lims);
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
     // A bounded wait; once one ran out, every later wait of the CTA gives up too.
     auto wait = [&](int bar, uint32_t parity) {
@@ -179,30 +215,29 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv8_prefill(const __grid_consta
         flag(p.a.status, kStatusTimeout);
         return false;
     };
+    auto wait_warp = [&](int bar, uint32_t parity) { return (bool)__all_sync(0xFFFFFFFFu, wait(bar, parity)); };
 
     if (tid == 0) {
-        tc::mbar_init(bars + kQ, 256);
+        tc::mbar_init(bars + kQ, kSoftmax);
         for (int i = 0; i < 2; ++i) {
-            tc::mbar_init(bars + kKFull + i, 128);
+            tc::mbar_init(bars + kKFull + i, kConv);
             tc::mbar_init(bars + kKEmpty + i, 1);
-            tc::mbar_init(bars + kVFull + i, 128);
+            tc::mbar_init(bars + kVFull + i, kConv);
             tc::mbar_init(bars + kVEmpty + i, 1);
             tc::mbar_init(bars + kS + i, 1);
-            tc::mbar_init(bars + kP + i, 128);
+            tc::mbar_init(bars + kP + i, kSoftmax / 2);
+            tc::mbar_init(bars + kLFull + i, 1);
+            tc::mbar_init(bars + kLEmpty + i, kConv);
         }
         tc::mbar_init(bars + kO, 1);
         tc::mbar_init(bars + kDrain, 1);
         tc::fence_mbar_init();
-        misc[1] = 0;
+        misc[1] = misc[2] = misc[3] = 0;
     }
     pdl_begin();
-    if (warp == 12) tc::tmem_alloc(const_cast<uint32_t*>(misc), 512);
+    if (warp == kMmaWarp) tc::tmem_alloc(const_cast<uint32_t*>(misc), 512);
     const Line line(p);
     const int64_t total = line_sums(line, sums, blockIdx.x == 0 ? p.a.status : nullptr);
-    tc::fence_before_sync();
-    __syncthreads();
-    tc::fence_after_sync();
-    const uint32_t tmem = misc[0];
     const int64_t share = total < p.ctas ? (total < 1 ? 1 : total) : p.ctas;
     int* desc = reinterpret_cast<int*>(p.a.part + ((int64_t)blockIdx.x * 2 + 1) * Part<D>::kFloats + Part<D>::kDesc);
     if (tid == 0) desc[4] = 0;
@@ -210,65 +245,87 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv8_prefill(const __grid_consta
     const int64_t u0 = any ? total * blockIdx.x / share : 0, u1 = any ? total * (blockIdx.x + 1) / share : 0;
     Cursor cur;
     if (any) line_find(line, sums, u0, cur);
+    tc::fence_before_sync();
+    __syncthreads();   // TMEM is there, the barriers are, and `sums` becomes the codes' place
+    tc::fence_after_sync();
+    const uint32_t tmem = misc[0];
 
-    if (wg < 2) {
-        // ---------------------------------------------------------------- softmax: row wt of tile wg
+    // registers by role: 4 * 96 + 56 + 40 = 6 * 80, what the CTA is launched with
+    if (warp < 16) {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 96;");
+        // ---------------------------------------------------------------- softmax: half `half` of a row of tile `t`
+        const int G = p.G, T = p.a.q.T, H = p.a.q.H;
+        const int t = warp >> 3, half = (warp >> 2) & 1, rt = (warp & 3) * 32 + lane;
         const uint32_t lanes = tmem + ((uint32_t)((warp & 3) * 32) << 16);
-        const uint32_t col_s = lanes + wg * 128, col_o = lanes + kColO + wg * D;
+        const uint32_t col_s = lanes + t * 128, col_o = lanes + kColO + t * D + half * (D / 2);
+        volatile float* xch = reinterpret_cast<volatile float*>(smem + S::xch) + t * 256;
+        // both halves of every row are here; false for all of them once one of them failed
+        auto agree = [&](bool ok) {
+            if (!ok) misc[2 + t] = 1;
+            asm volatile("bar.sync %0, 256;" ::"r"(1 + t) : "memory");
+            return misc[2 + t] == 0;
+        };
         uint32_t tile = 0, s_phase = 0, o_phase = 0;   // tiles done by the CTA; parities
         bool ok = true;
-        for (int64_t u = u0; u < u1 && ok;) {
+        for (int64_t u = u0; u < u1;) {
             const bool from_start = cur.step == 0;
             const int left = cur.steps - cur.step;
             const int todo = u1 - u < left ? (int)(u1 - u) : left;
-            const bool to_end = todo == left, used = wg * kTileRows < cur.rows;
-            const int row = wg * kTileRows + wt;
+            const bool to_end = todo == left, used = t * kTileRows < cur.rows;
+            const int row = t * kTileRows + rt;
             const bool mine = row < cur.rows;
             const int j = (cur.row0 + row) / G, g = cur.row0 + row - j * G;
             const int pos = mine ? cur.L - cur.n + j : -1;
             const int first = p.a.window ? pos - p.a.window + 1 : 0;
             float zs = p.a.sm_scale * 1.4426950408889634f;
-            {   // the query row as fp16, K-major; bf16 scaled by the power of two that takes its greatest
-                // finite magnitude to [2^14, 2^15)
+            {   // half a query row as fp16, K-major; bf16 scaled by the power of two that takes the row's
+                // greatest finite magnitude to [2^14, 2^15)
+                constexpr int kVec = D / 16;
                 const uint16_t* src = static_cast<const uint16_t*>(p.a.q.q) + (int64_t)cur.b * p.a.q.stride_b +
-                                      (int64_t)j * p.a.q.stride_t + (int64_t)(cur.h * G + g) * D;
-                uint8_t* dst = smem + S::q + wg * S::kTile;
-                float up = 1.0f;
+                                      (int64_t)j * p.a.q.stride_t + (int64_t)(cur.h * G + g) * D + half * (D / 2);
+                uint4 x[kVec];
+#pragma unroll
+                for (int i = 0; i < kVec; ++i) {
+                    x[i] = make_uint4(0, 0, 0, 0);
+                    if (mine) x[i] = __ldg(reinterpret_cast<const uint4*>(src) + i);
+                }
                 if (p.a.q.is_bf16) {
                     float amax = 0.0f;
-                    if (mine) {
-#pragma unroll 4
-                        for (int i = 0; i < D / 8; ++i) {
-                            const uint4 x = __ldg(reinterpret_cast<const uint4*>(src) + i);
-                            const uint32_t w[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
-                            for (int q = 0; q < 4; ++q) {
-                                const float a = fabsf(__uint_as_float(w[q] << 16)), b = fabsf(__uint_as_float(w[q] & 0xFFFF0000u));
-                                if (a <= 3.4028235e38f) amax = fmaxf(amax, a);
-                                if (b <= 3.4028235e38f) amax = fmaxf(amax, b);
-                            }
+                    for (int i = 0; i < kVec; ++i) {
+                        const uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+#pragma unroll
+                        for (int q = 0; q < 4; ++q) {
+                            const float a = fabsf(__uint_as_float(w[q] << 16)), b = fabsf(__uint_as_float(w[q] & 0xFFFF0000u));
+                            if (a <= 3.4028235e38f) amax = fmaxf(amax, a);
+                            if (b <= 3.4028235e38f) amax = fmaxf(amax, b);
                         }
                     }
+                    ok = agree(ok);              // the sums of the item before have been read
+                    xch[half * 128 + rt] = amax;
+                    ok = agree(ok);
+                    amax = fmaxf(amax, xch[(half ^ 1) * 128 + rt]);
                     int e = 14 - ((int)(__float_as_uint(amax) >> 23) - 127);
                     e = e > 126 ? 126 : e;
-                    up = exp2_int(e);
+                    const float up = exp2_int(e);
                     zs *= exp2_int(-e);
-                }
-#pragma unroll 4
-                for (int i = 0; i < D / 8; ++i) {
-                    uint4 x = make_uint4(0, 0, 0, 0);
-                    if (mine) x = __ldg(reinterpret_cast<const uint4*>(src) + i);
-                    if (p.a.q.is_bf16) {
-                        uint32_t w[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+                    for (int i = 0; i < kVec; ++i) {
+                        uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
 #pragma unroll
                         for (int q = 0; q < 4; ++q) {
                             const __half2 h = __floats2half2_rn(__uint_as_float(w[q] << 16) * up,
                                                                 __uint_as_float(w[q] & 0xFFFF0000u) * up);
                             memcpy(&w[q], &h, 4);
                         }
-                        x = make_uint4(w[0], w[1], w[2], w[3]);
+                        x[i] = make_uint4(w[0], w[1], w[2], w[3]);
                     }
-                    *reinterpret_cast<uint4*>(dst + (i >> 3) * S::kPanel + tc::sw128_offset(wt, i & 7)) = x;
+                }
+                uint8_t* dst = smem + S::q + t * S::kTile;
+#pragma unroll
+                for (int i = 0; i < kVec; ++i) {
+                    const int c = half * kVec + i;
+                    *reinterpret_cast<uint4*>(dst + (c >> 3) * S::kPanel + tc::sw128_offset(rt, c & 7)) = x[i];
                 }
                 tc::fence_proxy_async_smem();
                 tc::mbar_arrive(bars + kQ);
@@ -276,112 +333,112 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv8_prefill(const __grid_consta
             float M = kNone, l = 0.0f, e0 = 0.0f;
             for (int i = 0; i < todo; ++i, ++tile) {
                 if (!used) continue;
-                const int t0 = cur.lo + (cur.step + i) * kPos;
-                ok = __all_sync(0xFFFFFFFFu, wait(kS + wg, s_phase));
-                if (!ok) break;
+                const int t0 = cur.lo + (cur.step + i) * kPos + half * 64;
+                ok = wait_warp(kS + t, s_phase) && ok;
                 s_phase ^= 1;
                 tc::fence_after_sync();
-                const float2* f2 = sc + (tile & 3) * 8;
+                const float2* f2 = sc + (tile & 7) * 8 + half * 4;
+                uint32_t r[64];
+                tc::tmem_ld32_nowait(col_s + half * 64, r);
+                tc::tmem_ld32_nowait(col_s + half * 64 + 32, r + 32);
                 if (i == 0) {
-                    e0 = f2[0].y;
+                    e0 = sc[(tile & 7) * 8].y;
                     e0 = e0 < -100.0f ? -100.0f : (e0 > 100.0f ? 100.0f : e0);
                 }
-                const bool full = __all_sync(0xFFFFFFFFu, (!mine) || (t0 + kPos - 1 <= pos && t0 >= first));
+                // (factor of the logits, log2 of the value scale) of 16 positions
+                auto block = [&](int q) {
+                    const float2 f = f2[q];
+                    return make_float2(zs * f.x, f.y == -120.0f ? e0 : f.y);
+                };
+                tc::tmem_ld_wait();
+                if (!__all_sync(0xFFFFFFFFu, !mine || (t0 + 63 <= pos && t0 >= first))) {
+#pragma unroll
+                    for (int x = 0; x < 64; ++x)
+                        if (t0 + x > pos || t0 + x < first) r[x] = 0xFF800000u;
+                }
                 // ---- the greatest logit + log2(value scale) of the row
                 float top = -INFINITY;
 #pragma unroll
                 for (int q = 0; q < 4; ++q) {
-                    uint32_t r[32];
-                    tc::tmem_ld32_nowait(col_s + q * 32, r);
-                    tc::tmem_ld_wait();
+                    float m = fmaxf(__uint_as_float(r[q * 16]), __uint_as_float(r[q * 16 + 1]));
 #pragma unroll
-                    for (int hb = 0; hb < 2; ++hb) {
-                        const float2 f = f2[q * 2 + hb];
-                        const float ev = f.y == -120.0f ? e0 : f.y;
-                        float m = -INFINITY;
-                        if (full) {
-#pragma unroll
-                            for (int x = 0; x < 16; ++x) m = fmaxf(m, __uint_as_float(r[hb * 16 + x]));
-                        } else {
-#pragma unroll
-                            for (int x = 0; x < 16; ++x) {
-                                const int t = t0 + q * 32 + hb * 16 + x;
-                                if (t <= pos && t >= first) m = fmaxf(m, __uint_as_float(r[hb * 16 + x]));
-                            }
-                        }
-                        top = fmaxf(top, m * (zs * f.x) + ev);
-                    }
+                    for (int x = 2; x < 16; x += 2)
+                        m = max3(m, __uint_as_float(r[q * 16 + x]), __uint_as_float(r[q * 16 + x + 1]));
+                    const float2 f = block(q);
+                    top = fmaxf(top, m * f.x + f.y);
                 }
+                xch[half * 128 + rt] = top;
+                ok = agree(ok);      // and all of S is in registers: the weights may go over it
+                if (!ok) break;
+                top = fmaxf(top, xch[(half ^ 1) * 128 + rt]);
                 if (__any_sync(0xFFFFFFFFu, top > M + kLazy)) {
                     const float M1 = fmaxf(M, top), f = ex2(M - M1);
                     l *= f;
                     M = M1;
                     if (i > 0) {
-#pragma unroll
-                        for (int q = 0; q < D / 32; ++q) {
-                            uint32_t r[32];
-                            tc::tmem_ld32_nowait(col_o + q * 32, r);
+#pragma unroll 1
+                        for (int q = 0; q < D / 2; q += 16) {
+                            uint32_t o[16];
+                            tc::tmem_ld16_nowait(col_o + q, o);
                             tc::tmem_ld_wait();
 #pragma unroll
-                            for (int x = 0; x < 32; ++x) r[x] = __float_as_uint(__uint_as_float(r[x]) * f);
-                            tc::tmem_st32_nowait(col_o + q * 32, r);
+                            for (int x = 0; x < 16; ++x) o[x] = __float_as_uint(__uint_as_float(o[x]) * f);
+                            tc::tmem_st16_nowait(col_o + q, o);
                         }
                     }
                 }
                 // ---- weights over S, two to a column
 #pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    uint32_t r[32], w[16];
-                    tc::tmem_ld32_nowait(col_s + q * 32, r);
-                    tc::tmem_ld_wait();
+                for (int q = 0; q < 2; ++q) {
+                    uint32_t w[16];
 #pragma unroll
                     for (int hb = 0; hb < 2; ++hb) {
-                        const float2 f = f2[q * 2 + hb];
-                        const float ev = f.y == -120.0f ? e0 : f.y;
-                        const float a = zs * f.x, d = ev - M + kHeadroom;
-                        float sum = 0.0f;
+                        const uint32_t* v = r + q * 32 + hb * 16;
+                        const float2 f = block(q * 2 + hb);
+                        const float d = f.y - M + kHeadroom;
+                        const uint64_t ff = pack2(f.x, f.x), dd = pack2(d, d);
+                        uint64_t sum = 0;
 #pragma unroll
                         for (int x = 0; x < 16; x += 2) {
-                            const int t = t0 + q * 32 + hb * 16 + x;
-                            float w0 = ex2(__uint_as_float(r[hb * 16 + x]) * a + d);
-                            float w1 = ex2(__uint_as_float(r[hb * 16 + x + 1]) * a + d);
-                            if (!full) {
-                                if (!(t <= pos && t >= first)) w0 = 0.0f;
-                                if (!(t + 1 <= pos && t + 1 >= first)) w1 = 0.0f;
-                            }
-                            sum += w0 + w1;
-                            const __half2 h = __floats2half2_rn(w0, w1);
+                            const uint64_t z = fma2(pack2(__uint_as_float(v[x]), __uint_as_float(v[x + 1])), ff, dd);
+                            const float2 zz = unpack2(z), e = make_float2(ex2(zz.x), ex2(zz.y));
+                            sum = add2(sum, pack2(e.x, e.y));
+                            const __half2 h = __floats2half2_rn(e.x, e.y);
                             memcpy(&w[hb * 8 + x / 2], &h, 4);
                         }
                         // back from 2^(z + log2 vs - M + 8) to 2^(z + e0 - M + 8), exactly
-                        const float de = e0 - ev;
-                        l += sum * exp2_int(de < -126.0f ? -126 : (de > 126.0f ? 126 : (int)de));
+                        const float de = e0 - f.y;
+                        const float2 s2 = unpack2(sum);
+                        l += (s2.x + s2.y) * exp2_int(de < -126.0f ? -126 : (de > 126.0f ? 126 : (int)de));
                     }
-                    tc::tmem_st16_nowait(col_s + q * 16, w);
+                    tc::tmem_st16_nowait(col_s + half * 32 + q * 16, w);
                 }
                 tc::tmem_st_wait();
                 tc::fence_before_sync();
-                tc::mbar_arrive(bars + kP + wg);
+                tc::mbar_arrive(bars + kP + t);
             }
-            if (!ok) break;
-            // ---- the outputs
-            ok = __all_sync(0xFFFFFFFFu, wait(kO, o_phase));
-            if (!ok) break;
+            // ---- the outputs, half the channels
+            ok = ok && wait_warp(kO, o_phase);
             o_phase ^= 1;
             tc::fence_after_sync();
+            xch[half * 128 + rt] = l;
+            ok = agree(ok);
+            if (!ok) break;
+            l = half ? xch[rt] + l : l + xch[128 + rt];
             const bool whole = from_start && to_end;
             float* part = p.a.part + ((int64_t)blockIdx.x * 2 + (from_start ? 1 : 0)) * Part<D>::kFloats;
             const int64_t at = ((int64_t)cur.b * T + j) * H + cur.h * G + g;
             const float f = l == 0.0f ? 0.0f : exp2_int((int)e0) / l;
             if (used) {
-#pragma unroll
-                for (int q = 0; q < D / 32; ++q) {
+#pragma unroll 1
+                for (int q = 0; q < D / 2; q += 32) {
                     uint32_t r[32];
-                    tc::tmem_ld32_nowait(col_o + q * 32, r);
+                    tc::tmem_ld32_nowait(col_o + q, r);
                     tc::tmem_ld_wait();
                     if (!mine) continue;
+                    const int ch = half * (D / 2) + q;
                     if (whole) {
-                        uint4* dst = reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.a.out) + at * D + q * 32);
+                        uint4* dst = reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.a.out) + at * D + ch);
 #pragma unroll
                         for (int x = 0; x < 4; ++x) {
                             uint32_t w[4];
@@ -400,14 +457,14 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv8_prefill(const __grid_consta
                         }
                     } else {
                         // by 16-byte columns across the rows, so that a warp's stores are dense
-                        float4* dst = reinterpret_cast<float4*>(part) + (int64_t)q * 8 * kRows + row;
+                        float4* dst = reinterpret_cast<float4*>(part) + (int64_t)(ch / 4) * kRows + row;
 #pragma unroll
                         for (int x = 0; x < 8; ++x)
                             dst[x * kRows] = make_float4(__uint_as_float(r[x * 4]), __uint_as_float(r[x * 4 + 1]),
                                                          __uint_as_float(r[x * 4 + 2]), __uint_as_float(r[x * 4 + 3]));
                     }
                 }
-                if (mine) {
+                if (mine && half == 0) {
                     if (whole) {
                         if (p.a.lse)
                             p.a.lse[at] = l == 0.0f ? -INFINITY : (M - e0 - kHeadroom + log2f(l)) * 0.6931471805599453f;
@@ -433,172 +490,179 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv8_prefill(const __grid_consta
             cur.step += todo - 1;
             if (++cur.step >= cur.steps) line.next_item(cur);
         }
-    } else if (wg == 2) {
+    } else if (warp < kMmaWarp) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
         // ---------------------------------------------------------------- codes to fp16 operand tiles
-        constexpr int kPer = D / 16;             // 16-byte pieces of a row, and of this thread in a tile
-        uint32_t tile = 0, k_phase = 0, v_phase = 0;
-        uint4 kr[kPer], vr[kPer];
-        int phys[kPer];
-        float ks = 0.0f, vs = 1.0f;
-        int t0 = 0, lim = 0, h = 0, my_phys = -1;
-        int64_t ahead_u = u0;
-        // the blocks of the tile at `cur`, which moves on
-        auto look = [&]() {
-            t0 = cur.lo + cur.step * kPos;
-            lim = cur.L;
-            h = cur.h;
-            my_phys = -1;
-#pragma unroll
-            for (int i = 0; i < kPer; ++i) phys[i] = -1;
-            if (ahead_u >= u1) return;
-#pragma unroll
-            for (int i = 0; i < kPer; ++i) {
-                const int t = t0 + (i * 128 + wt) / kPer;
-                if (t < lim) {
-                    phys[i] = kv8_block(p.c, cur.b, t >> p.c.bs_log2);
-                    if (phys[i] < 0) flag(p.a.status, kStatusBounds);
-                }
-            }
-            if (wt < 8 && t0 + wt * 16 < lim) my_phys = kv8_block(p.c, cur.b, (t0 + wt * 16) >> p.c.bs_log2);
-            ++ahead_u;
-            if (++cur.step >= cur.steps) line.next_item(cur);
-        };
-        auto fetch = [&](uint4 (&r)[kPer], const uint8_t* codes) {
-#pragma unroll
-            for (int i = 0; i < kPer; ++i) {
-                const int x = i * 128 + wt, t = t0 + x / kPer;
-                r[i] = make_uint4(0, 0, 0, 0);      // behind the sequence's end: zeros, whatever the block holds
-                if (phys[i] >= 0) {
-                    const int64_t row = (((int64_t)phys[i] * p.c.heads + h) << p.c.bs_log2) + (t & (bs - 1));
-                    r[i] = __ldg(reinterpret_cast<const uint4*>(codes + row * D) + x % kPer);
-                }
-            }
-        };
-        auto store = [&](const uint4 (&r)[kPer], uint8_t* dst) {
-#pragma unroll
-            for (int i = 0; i < kPer; ++i) {
-                const int x = i * 128 + wt, row = x / kPer, piece = x % kPer;
-                const uint32_t w[4] = {r[i].x, r[i].y, r[i].z, r[i].w};
-                uint4 a, b;
-                a.x = half2_lo(w[0]), a.y = half2_hi(w[0]), a.z = half2_lo(w[1]), a.w = half2_hi(w[1]);
-                b.x = half2_lo(w[2]), b.y = half2_hi(w[2]), b.z = half2_lo(w[3]), b.w = half2_hi(w[3]);
-                uint8_t* panel = dst + (piece >> 2) * S::kPanel;
-                const uint32_t c0 = (piece & 3) * 2;
-                // the two panels share banks: their pieces go in opposite order
-                if (piece & 4) {
-                    *reinterpret_cast<uint4*>(panel + tc::sw128_offset(row, c0 + 1)) = b;
-                    *reinterpret_cast<uint4*>(panel + tc::sw128_offset(row, c0)) = a;
-                } else {
-                    *reinterpret_cast<uint4*>(panel + tc::sw128_offset(row, c0)) = a;
-                    *reinterpret_cast<uint4*>(panel + tc::sw128_offset(row, c0 + 1)) = b;
-                }
-            }
-        };
-        auto scales = [&]() {
-            ks = 0.0f;
-            vs = 1.0f;
-            if (my_phys >= 0) {
-                const int64_t unit = (int64_t)my_phys * p.c.heads + h;
-                ks = __ldg(p.c.k_scale + unit);
-                vs = __ldg(p.c.v_scale + unit);
-            }
-        };
-        bool ok = true;
-        if (u0 < u1) {
-            look();
-            fetch(kr, p.c.k);
-            fetch(vr, p.c.v);
-            scales();
-        }
-        for (int64_t u = u0; u < u1; ++u, ++tile) {
-            const uint32_t st = tile & 1;
-            if (tile >= 2) {
-                ok = __all_sync(0xFFFFFFFFu, wait(kKEmpty + st, (k_phase >> st) & 1u));
-                if (!ok) break;
-                k_phase ^= 1u << st;
-            }
-            store(kr, smem + S::k + st * S::kTile);
-            if (wt < 8) sc[(tile & 3) * 8 + wt] = make_float2(ks, (float)((int)(__float_as_uint(vs) >> 23) - 127));
-            tc::fence_proxy_async_smem();
-            tc::mbar_arrive(bars + kKFull + st);
-            look();
-            fetch(kr, p.c.k);
-            scales();
-            if (tile >= 2) {
-                ok = __all_sync(0xFFFFFFFFu, wait(kVEmpty + st, (v_phase >> st) & 1u));
-                if (!ok) break;
-                v_phase ^= 1u << st;
-            }
-            store(vr, smem + S::v + st * S::kTile);
-            tc::fence_proxy_async_smem();
-            tc::mbar_arrive(bars + kVFull + st);
-            fetch(vr, p.c.v);
-        }
-    } else if (warp == 12 && lane == 0) {
-        // ---------------------------------------------------------------- every tcgen05.mma of the CTA
-        constexpr uint32_t idesc_s = tc::idesc_f16_f32(128, kPos);
-        constexpr uint32_t idesc_o = tc::idesc_f16_f32(128, D, false, true);
-        const uint64_t dq = tc::desc_sw128(tc::smem_u32(smem + S::q)), dk = tc::desc_sw128(tc::smem_u32(smem + S::k));
-        const uint64_t dv = tc::desc_mn_sw128(tc::smem_u32(smem + S::v), S::kPanel, 1024);
-        uint32_t tile = 0, q_phase = 0, p_phase = 0;
-        bool ok = true;
-        auto scores = [&](int t, uint32_t st) {      // S_t = Q_t K^T
-#pragma unroll
+        const int ct = tid - kSoftmax, l8 = ct & 7;
+        // Piece (16 codes, two 16-byte chunks of fp16) `x` of this thread: eight lanes load 128 dense bytes'
+        // worth of distinct banks and store to eight distinct ones.
+        auto convert = [&](const uint8_t* src, uint8_t* dst, int lim) {
+#pragma unroll 4
             for (int x = 0; x < D / 16; ++x) {
-                const uint32_t off = (x >> 2) * S::kPanel + (x & 3) * 32;
-                tc::mma_f16(tmem + t * 128, tc::desc_at(dq, t * S::kTile + off), tc::desc_at(dk, st * S::kTile + off), idesc_s, x > 0);
+                const int row = D == 128 ? 2 * ((ct >> 3) + 16 * (x >> 1)) + ((l8 >> 2) ^ (x & 1)) : (ct >> 2) + 32 * x;
+                const int piece = D == 128 ? l8 : ct & 3;
+                uint4 w = *reinterpret_cast<const uint4*>(src + row * D + piece * 16);
+                if (row >= lim) w = make_uint4(0, 0, 0, 0);   // behind the sequence's end: zeros, whatever is there
+                uint8_t* panel = dst + (piece >> 2) * S::kPanel;
+                const uint32_t c = (piece & 3) * 2;
+                *reinterpret_cast<uint4*>(panel + tc::sw128_offset(row, c)) =
+                    make_uint4(half2_lo(w.x), half2_hi(w.x), half2_lo(w.y), half2_hi(w.y));
+                *reinterpret_cast<uint4*>(panel + tc::sw128_offset(row, c + 1)) =
+                    make_uint4(half2_lo(w.z), half2_hi(w.z), half2_lo(w.w), half2_hi(w.w));
             }
         };
-        auto outputs = [&](int t, uint32_t st, bool more) {   // O_t += P_t V
-#pragma unroll
-            for (int x = 0; x < kPos / 16; ++x)
-                tc::mma_f16_ta(tmem + kColO + t * D, tmem + t * 128 + x * 8, tc::desc_at(dv, st * S::kTile + x * 2048), idesc_o,
-                               more || x > 0);
-        };
-        for (int64_t u = u0; u < u1 && ok;) {
-            const int left = cur.steps - cur.step;
-            const int todo = u1 - u < left ? (int)(u1 - u) : left;
-            const int tiles = cur.rows > kTileRows ? 2 : 1;
-            ok = wait(kQ, q_phase);
-            q_phase ^= 1;
-            for (int i = 0; i <= todo && ok; ++i) {
-                const uint32_t st = tile & 1, prev = st ^ 1;     // stage of tile i, and of tile i - 1
-                if (i < todo) ok = wait(kKFull + st, (tile >> 1) & 1u);
-                if (i > 0) ok = ok && wait(kVFull + prev, ((tile - 1) >> 1) & 1u);
-                for (int t = 0; t < tiles && ok; ++t) {
-                    if (i > 0) {
-                        ok = wait(kP + t, (p_phase >> t) & 1u);
-                        if (!ok) break;
-                        p_phase ^= 1u << t;
-                        tc::fence_after_sync();
-                        outputs(t, prev, i > 1);
-                        if (t == tiles - 1) tc::mma_commit(bars + kVEmpty + prev);
-                    } else {
-                        tc::fence_after_sync();
-                    }
-                    if (i < todo) {
-                        scores(t, st);
-                        tc::mma_commit(bars + kS + t);
-                        if (t == tiles - 1) tc::mma_commit(bars + kKEmpty + st);
-                    }
-                }
-                if (i < todo) ++tile;
-            }
-            if (ok) tc::mma_commit(bars + kO);
-            u += todo;
-            cur.step += todo - 1;
-            if (++cur.step >= cur.steps) line.next_item(cur);
+        const int steps = (int)(u1 - u0);
+        for (int tile = 0; tile < steps; ++tile) {
+            const uint32_t st = tile & 1;
+            bool ok = wait_warp(kLFull, st);
+            if (tile >= 2) ok = ok && wait_warp(kKEmpty + st, ((tile >> 1) - 1) & 1);
+            if (!ok) break;
+            const int lim = lims[tile & 7];
+            convert(smem + S::codes, smem + S::k + st * S::kTile, lim);
+            tc::fence_proxy_async_smem();
+            tc::mbar_arrive(bars + kLEmpty);
+            tc::mbar_arrive(bars + kKFull + st);
+            ok = wait_warp(kLFull + 1, st);
+            if (tile >= 2) ok = ok && wait_warp(kVEmpty + st, ((tile >> 1) - 1) & 1);
+            if (!ok) break;
+            convert(smem + S::codes + kPos * D, smem + S::v + st * S::kTile, lim);
+            tc::fence_proxy_async_smem();
+            tc::mbar_arrive(bars + kLEmpty + 1);
+            tc::mbar_arrive(bars + kVFull + st);
         }
-        if (!ok) {
-            // the products already issued still write: a last commit, waited for with the full limit
-            tc::mma_commit(bars + kDrain);
-            tc::mbar_wait(bars + kDrain, 0);
+    } else {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 40;");
+        if (warp == kLoadWarp) {
+            // ------------------------------------------------------------ pages, scales and the codes' loads
+            const int box = p.c.bs() < kPos ? p.c.bs() : kPos, boxes = kPos / box;
+            uint32_t issued = 0, steps = (uint32_t)(u1 - u0);
+            int phys = -1, lim = 0, h = 0;
+            auto look = [&](bool there) {    // lane x < 8: the block of positions 16 x .. of the tile at `cur`
+                phys = -1;
+                if (!there) return;
+                const int t0 = cur.lo + cur.step * kPos;
+                lim = cur.L - t0;
+                h = cur.h;
+                if (lane < 8 && lane * 16 < lim) {
+                    phys = kv8_block(p.c, cur.b, (t0 + lane * 16) >> p.c.bs_log2);
+                    if (phys < 0) flag(p.a.status, kStatusBounds);
+                }
+                if (++cur.step >= cur.steps) line.next_item(cur);
+            };
+            bool ok = true;
+            if (steps) look(true);
+            for (uint32_t tile = 0; tile < steps; ++tile) {
+                const int now = phys, now_h = h, now_lim = lim;
+                look(tile + 1 < steps);
+                float ks = 1.0f, vs = 1.0f;
+                if (now >= 0) {
+                    const int64_t unit = (int64_t)now * p.c.heads + now_h;
+                    ks = __ldg(p.c.k_scale + unit);
+                    vs = __ldg(p.c.v_scale + unit);
+                }
+                // lane x < boxes copies box x: the block of its first 16 positions
+                const int mine = __shfl_sync(0xFFFFFFFFu, now, (lane * (box / 16)) & 7);
+                const bool copy = lane < boxes && mine >= 0;
+                const uint32_t n = __popc(__ballot_sync(0xFFFFFFFFu, copy));
+                const int row = copy ? (mine * p.c.heads + now_h) << p.c.bs_log2 : 0;
+#pragma unroll
+                for (int kv = 0; kv < 2 && ok; ++kv) {
+                    if (tile >= 1) ok = wait_warp(kLEmpty + kv, (tile - 1) & 1);
+                    if (!ok) break;
+                    if (kv == 0) {
+                        if (lane < 8) sc[(tile & 7) * 8 + lane] = make_float2(ks, (float)((int)(__float_as_uint(vs) >> 23) - 127));
+                        if (lane == 0) lims[tile & 7] = now_lim;
+                        __syncwarp();
+                    }
+                    if (lane == 0) tc::mbar_arrive_expect_tx(bars + kLFull + kv, n * box * D);
+                    __syncwarp();
+                    if (copy)
+                        tc::tma_load_2d(smem + S::codes + kv * kPos * D + lane * box * D, kv ? &vmap : &kmap, 0, row, bars + kLFull + kv);
+                    __syncwarp();
+                    ++issued;
+                }
+                if (!ok) break;
+            }
+            // loads that nobody waits for any more still land in this CTA's memory
+            for (int kv = 0; kv < 2; ++kv) {
+                const uint32_t done = (issued + 1 - kv) / 2;
+                if (done) tc::mbar_wait(bars + kLFull + kv, (done - 1) & 1);
+            }
+        } else if (warp == kMmaWarp) {
+            // ------------------------------------------------------------ every tcgen05.mma of the CTA
+            constexpr uint32_t idesc_s = tc::idesc_f16_f32(128, kPos);
+            constexpr uint32_t idesc_o = tc::idesc_f16_f32(128, D, false, true);
+            const uint64_t dq = tc::desc_sw128(tc::smem_u32(smem + S::q)), dk = tc::desc_sw128(tc::smem_u32(smem + S::k));
+            const uint64_t dv = tc::desc_mn_sw128(tc::smem_u32(smem + S::v), S::kPanel, 1024);
+            const uint32_t tmem0 = __shfl_sync(0xFFFFFFFFu, tmem, 0);
+            uint32_t tile = 0, q_phase = 0, p_phase = 0;
+            bool ok = true;
+            auto scores = [&](int t, uint32_t st) {      // S_t = Q_t K^T
+#pragma unroll
+                for (int x = 0; x < D / 16; ++x) {
+                    const uint32_t off = (x >> 2) * S::kPanel + (x & 3) * 32;
+                    tc::mma_f16(tmem0 + t * 128, tc::desc_at(dq, t * S::kTile + off), tc::desc_at(dk, st * S::kTile + off), idesc_s, x > 0);
+                }
+            };
+            auto outputs = [&](int t, uint32_t st, bool more) {   // O_t += P_t V
+#pragma unroll
+                for (int x = 0; x < kPos / 16; ++x)
+                    tc::mma_f16_ta(tmem0 + kColO + t * D, tmem0 + t * 128 + x * 8, tc::desc_at(dv, st * S::kTile + x * 2048), idesc_o,
+                                   more || x > 0);
+            };
+            for (int64_t u = u0; u < u1 && ok;) {
+                const int left = cur.steps - cur.step;
+                const int todo = __shfl_sync(0xFFFFFFFFu, u1 - u < left ? (int)(u1 - u) : left, 0);
+                const int tiles = __shfl_sync(0xFFFFFFFFu, cur.rows > kTileRows ? 2 : 1, 0);
+                ok = wait_warp(kQ, q_phase);
+                q_phase ^= 1;
+                for (int i = 0; i <= todo && ok; ++i) {
+                    const uint32_t st = tile & 1, prev = st ^ 1;     // stage of tile i, and of tile i - 1
+                    if (i < todo) ok = wait_warp(kKFull + st, (tile >> 1) & 1u);
+                    if (i > 0) ok = ok && wait_warp(kVFull + prev, ((tile - 1) >> 1) & 1u);
+                    for (int t = 0; t < tiles && ok; ++t) {
+                        if (i > 0) {
+                            ok = wait_warp(kP + t, (p_phase >> t) & 1u);
+                            if (!ok) break;
+                            p_phase ^= 1u << t;
+                            tc::fence_after_sync();
+                            if (tc::elect_one()) {
+                                outputs(t, prev, i > 1);
+                                if (t == tiles - 1) tc::mma_commit(bars + kVEmpty + prev);
+                            }
+                            __syncwarp();
+                        } else {
+                            tc::fence_after_sync();
+                        }
+                        if (i < todo) {
+                            if (tc::elect_one()) {
+                                scores(t, st);
+                                tc::mma_commit(bars + kS + t);
+                                if (t == tiles - 1) tc::mma_commit(bars + kKEmpty + st);
+                            }
+                            __syncwarp();
+                        }
+                    }
+                    if (i < todo) ++tile;
+                }
+                if (ok && tc::elect_one()) tc::mma_commit(bars + kO);
+                __syncwarp();
+                u += todo;
+                cur.step += todo - 1;
+                if (++cur.step >= cur.steps) line.next_item(cur);
+            }
+            if (!ok) {
+                // the products already issued still write: a last commit, waited for with the full limit
+                if (tc::elect_one()) tc::mma_commit(bars + kDrain);
+                __syncwarp();
+                tc::mbar_wait(bars + kDrain, 0);
+            }
         }
     }
     __syncwarp();
     tc::fence_before_sync();
     __syncthreads();
-    if (warp == 12) tc::tmem_dealloc(tmem, 512);
+    if (warp == kMmaWarp) tc::tmem_dealloc(tmem, 512);
 }
 
 // The items that the line's cuts went through: CTA x merges the item that
@@ -653,7 +717,10 @@ cudaError_t launch(const Params& p, cudaStream_t st) {
     static_assert(S::bytes <= 227 * 1024, "shared memory of a CTA");
     cudaError_t e = cudaFuncSetAttribute(k_kv8_prefill<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, S::bytes);
     if (e != cudaSuccess) return e;
-    e = launch_pdl(k_kv8_prefill<D>, p.ctas, kThreads, S::bytes, st, p);
+    CUtensorMap kmap, vmap;
+    const int box = p.c.bs() < kPos ? p.c.bs() : kPos;
+    if (!kv8_row_map(&kmap, p.c, p.c.k, box, false) || !kv8_row_map(&vmap, p.c, p.c.v, box, false)) return cudaErrorNotSupported;
+    e = launch_pdl(k_kv8_prefill<D>, p.ctas, kThreads, S::bytes, st, p, kmap, vmap);
     if (e != cudaSuccess) return e;
     return launch_pdl(k_kv8_prefill_combine<D>, dim3(p.ctas, D / 4), kRows, 0, st, p);
 }

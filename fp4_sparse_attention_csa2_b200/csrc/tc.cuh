@@ -130,8 +130,21 @@ __device__ __forceinline__ void mma_f16(uint32_t d_tmem, uint64_t a_desc, uint64
         : "memory");
 }
 
-// The same with A in tensor memory (one row a lane, two fp16 of consecutive k
-// per 32-bit column).
+// True in one lane of a converged warp.  A branch on it, unlike one on the lane
+// number, keeps the operands of the tcgen05 instructions inside in uniform
+// registers.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t e;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "elect.sync _|p, 0xFFFFFFFF;\n\t"
+        "selp.b32 %0, 1, 0, p;\n\t}"
+        : "=r"(e));
+    return e != 0;
+}
+
+// D[tmem] (+)= A[tmem] * B[smem]^T, kind::f16: A one row a lane, two fp16 of
+// consecutive k per 32-bit column.
 __device__ __forceinline__ void mma_f16_ta(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
                                            uint32_t accumulate) {
     asm volatile(
