@@ -259,7 +259,9 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv8_prefill(const __grid_consta
         const uint32_t lanes = tmem + ((uint32_t)((warp & 3) * 32) << 16);
         const uint32_t col_s = lanes + t * 128, col_o = lanes + kColO + t * D + half * (D / 2);
         volatile float* xch = reinterpret_cast<volatile float*>(smem + S::xch) + t * 256;
-        // both halves of every row are here; false for all of them once one of them failed
+        // both halves of the tile's rows are here; false for all of them once one failed.  (A barrier for
+        // each two warps that share 32 rows, 64 threads, was slower, 343 against 314 us for 2,048 tokens over
+        // 8,192 positions: warps of a tile that drift apart delay the tile's products.)
         auto agree = [&](bool ok) {
             if (!ok) misc[2 + t] = 1;
             asm volatile("bar.sync %0, 256;" ::"r"(1 + t) : "memory");
@@ -267,20 +269,35 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv8_prefill(const __grid_consta
         };
         uint32_t tile = 0, s_phase = 0, o_phase = 0;   // tiles done by the CTA; parities
         bool ok = true;
-        for (int64_t u = u0; u < u1;) {
-            const bool from_start = cur.step == 0;
-            const int left = cur.steps - cur.step;
-            const int todo = u1 - u < left ? (int)(u1 - u) : left;
-            const bool to_end = todo == left, used = t * kTileRows < cur.rows;
-            const int row = t * kTileRows + rt;
-            const bool mine = row < cur.rows;
-            const int j = (cur.row0 + row) / G, g = cur.row0 + row - j * G;
-            const int pos = mine ? cur.L - cur.n + j : -1;
-            const int first = p.a.window ? pos - p.a.window + 1 : 0;
+        // Between items only this much of the cursor is kept (registers): the rest is worked out again.
+        int pair = cur.pair, head = cur.h, step = cur.step, todo_all = (int)(u1 - u0);
+        auto item = [&]() {
+            asm volatile("" : "+r"(pair));   // not to be kept from the time before
+            Cursor k;
+            line.load(k, pair, nullptr);
+            k.h = head;
+            k.step = step;
+            return k;
+        };
+        const int row = t * kTileRows + rt;
+        while (todo_all > 0) {
+            int todo, pos, first;
+            bool used;
             float zs = p.a.sm_scale * 1.4426950408889634f;
             {   // half a query row as fp16, K-major; bf16 scaled by the power of two that takes the row's
                 // greatest finite magnitude to [2^14, 2^15)
                 constexpr int kVec = D / 16;
+                const Cursor cur = item();
+                todo = todo_all < cur.steps - cur.step ? todo_all : cur.steps - cur.step;
+                used = t * kTileRows < cur.rows;
+                const bool mine = row < cur.rows;
+                const int j = (cur.row0 + row) / G, g = cur.row0 + row - j * G;
+                pos = mine ? cur.L - cur.n + j : -1;
+                first = p.a.window ? pos - p.a.window + 1 : 0;
+                // as seen from this half's first column of the item's first step
+                pos -= cur.lo + cur.step * kPos + half * 64;
+                first -= cur.lo + cur.step * kPos + half * 64;
+                if (!mine) pos = 0x7FFFFFFF, first = -0x7FFFFFFF;   // rows without a token: anything, without the mask
                 const uint16_t* src = static_cast<const uint16_t*>(p.a.q.q) + (int64_t)cur.b * p.a.q.stride_b +
                                       (int64_t)j * p.a.q.stride_t + (int64_t)(cur.h * G + g) * D + half * (D / 2);
                 uint4 x[kVec];
@@ -333,7 +350,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv8_prefill(const __grid_consta
             float M = kNone, l = 0.0f, e0 = 0.0f;
             for (int i = 0; i < todo; ++i, ++tile) {
                 if (!used) continue;
-                const int t0 = cur.lo + (cur.step + i) * kPos + half * 64;
+                const int t0 = i * kPos;
                 ok = wait_warp(kS + t, s_phase) && ok;
                 s_phase ^= 1;
                 tc::fence_after_sync();
@@ -351,7 +368,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv8_prefill(const __grid_consta
                     return make_float2(zs * f.x, f.y == -120.0f ? e0 : f.y);
                 };
                 tc::tmem_ld_wait();
-                if (!__all_sync(0xFFFFFFFFu, !mine || (t0 + 63 <= pos && t0 >= first))) {
+                if (!__all_sync(0xFFFFFFFFu, t0 + 63 <= pos && t0 >= first)) {
 #pragma unroll
                     for (int x = 0; x < 64; ++x)
                         if (t0 + x > pos || t0 + x < first) r[x] = 0xFF800000u;
@@ -389,29 +406,26 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv8_prefill(const __grid_consta
                 }
                 // ---- weights over S, two to a column
 #pragma unroll
-                for (int q = 0; q < 2; ++q) {
-                    uint32_t w[16];
+                for (int q = 0; q < 4; ++q) {
+                    const uint32_t* v = r + q * 16;
+                    const float2 f = block(q);
+                    const float d = f.y - M + kHeadroom;
+                    const uint64_t ff = pack2(f.x, f.x), dd = pack2(d, d);
+                    uint64_t sum = 0;
+                    uint32_t w[8];
 #pragma unroll
-                    for (int hb = 0; hb < 2; ++hb) {
-                        const uint32_t* v = r + q * 32 + hb * 16;
-                        const float2 f = block(q * 2 + hb);
-                        const float d = f.y - M + kHeadroom;
-                        const uint64_t ff = pack2(f.x, f.x), dd = pack2(d, d);
-                        uint64_t sum = 0;
-#pragma unroll
-                        for (int x = 0; x < 16; x += 2) {
-                            const uint64_t z = fma2(pack2(__uint_as_float(v[x]), __uint_as_float(v[x + 1])), ff, dd);
-                            const float2 zz = unpack2(z), e = make_float2(ex2(zz.x), ex2(zz.y));
-                            sum = add2(sum, pack2(e.x, e.y));
-                            const __half2 h = __floats2half2_rn(e.x, e.y);
-                            memcpy(&w[hb * 8 + x / 2], &h, 4);
-                        }
-                        // back from 2^(z + log2 vs - M + 8) to 2^(z + e0 - M + 8), exactly
-                        const float de = e0 - f.y;
-                        const float2 s2 = unpack2(sum);
-                        l += (s2.x + s2.y) * exp2_int(de < -126.0f ? -126 : (de > 126.0f ? 126 : (int)de));
+                    for (int x = 0; x < 16; x += 2) {
+                        const float2 z = unpack2(fma2(pack2(__uint_as_float(v[x]), __uint_as_float(v[x + 1])), ff, dd));
+                        const float2 e = make_float2(ex2(z.x), ex2(z.y));
+                        sum = add2(sum, pack2(e.x, e.y));
+                        const __half2 h = __floats2half2_rn(e.x, e.y);
+                        memcpy(&w[x / 2], &h, 4);
                     }
-                    tc::tmem_st16_nowait(col_s + half * 32 + q * 16, w);
+                    // back from 2^(z + log2 vs - M + 8) to 2^(z + e0 - M + 8), exactly
+                    const float de = e0 - f.y;
+                    const float2 s2 = unpack2(sum);
+                    l += (s2.x + s2.y) * exp2_int(de < -126.0f ? -126 : (de > 126.0f ? 126 : (int)de));
+                    tc::tmem_st8_nowait(col_s + half * 32 + q * 8, w);
                 }
                 tc::tmem_st_wait();
                 tc::fence_before_sync();
@@ -425,6 +439,10 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv8_prefill(const __grid_consta
             ok = agree(ok);
             if (!ok) break;
             l = half ? xch[rt] + l : l + xch[128 + rt];
+            Cursor cur = item();
+            const bool mine = row < cur.rows;
+            const int j = (cur.row0 + row) / G, g = cur.row0 + row - j * G, left = cur.steps - cur.step;
+            const bool from_start = cur.step == 0, to_end = todo == left;
             const bool whole = from_start && to_end;
             float* part = p.a.part + ((int64_t)blockIdx.x * 2 + (from_start ? 1 : 0)) * Part<D>::kFloats;
             const int64_t at = ((int64_t)cur.b * T + j) * H + cur.h * G + g;
@@ -477,7 +495,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv8_prefill(const __grid_consta
                 }
             }
             if (from_start && !to_end && tid == 0) {
-                const int64_t last_u = u + left - 1;
+                const int64_t last_u = u1 - todo_all + left - 1;
                 const int64_t last = ((last_u + 1) * share + total - 1) / total - 1;
                 desc[0] = cur.b;
                 desc[1] = cur.h;
@@ -486,9 +504,13 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv8_prefill(const __grid_consta
                 desc[4] = (int)(last - blockIdx.x) + 1;
             }
             tc::fence_before_sync();
-            u += todo;
-            cur.step += todo - 1;
-            if (++cur.step >= cur.steps) line.next_item(cur);
+            todo_all -= todo;
+            if (todo_all > 0) {      // an item that goes on behind this piece is the last of it
+                line.next_item(cur);
+                pair = cur.pair;
+                head = cur.h;
+                step = 0;
+            }
         }
     } else if (warp < kMmaWarp) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
@@ -610,10 +632,22 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv8_prefill(const __grid_consta
                     tc::mma_f16_ta(tmem0 + kColO + t * D, tmem0 + t * 128 + x * 8, tc::desc_at(dv, st * S::kTile + x * 2048), idesc_o,
                                    more || x > 0);
             };
-            for (int64_t u = u0; u < u1 && ok;) {
-                const int left = cur.steps - cur.step;
-                const int todo = __shfl_sync(0xFFFFFFFFu, u1 - u < left ? (int)(u1 - u) : left, 0);
-                const int tiles = __shfl_sync(0xFFFFFFFFu, cur.rows > kTileRows ? 2 : 1, 0);
+            int pair = cur.pair, head = cur.h, step = cur.step, todo_all = (int)(u1 - u0);
+            while (todo_all > 0 && ok) {
+                int todo, tiles;
+                {
+                    line.load(cur, pair, nullptr);
+                    todo = cur.steps - step < todo_all ? cur.steps - step : todo_all;
+                    tiles = cur.rows > kTileRows ? 2 : 1;
+                    todo_all -= todo;
+                    cur.h = head;
+                    line.next_item(cur);
+                    pair = cur.pair;
+                    head = cur.h;
+                    step = 0;
+                }
+                todo = __shfl_sync(0xFFFFFFFFu, todo, 0);
+                tiles = __shfl_sync(0xFFFFFFFFu, tiles, 0);
                 ok = wait_warp(kQ, q_phase);
                 q_phase ^= 1;
                 for (int i = 0; i <= todo && ok; ++i) {
@@ -647,9 +681,6 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv8_prefill(const __grid_consta
                 }
                 if (ok && tc::elect_one()) tc::mma_commit(bars + kO);
                 __syncwarp();
-                u += todo;
-                cur.step += todo - 1;
-                if (++cur.step >= cur.steps) line.next_item(cur);
             }
             if (!ok) {
                 // the products already issued still write: a last commit, waited for with the full limit
