@@ -532,68 +532,74 @@ class KV8Cache:
         self.k, self.v, self.k_scale, self.v_scale, self.k_bounds = k, v, ks, vs, kb
         self.seq_lens, self.block_table = seq_lens, table
         self.batch, self.max_blocks, self.block_size, self.n_kv_heads, self.head_dim = batch, max_blocks, bs, heads, dim
-        self.device = k.device
+        self.device, self.index = k.device, k.get_device()
         self.c = csa2_kv8_cache(_addr(k), _addr(v), _addr(ks), _addr(vs), _addr(kb), _addr(table), _addr(seq_lens),
                                 batch, max_blocks, bs, heads, dim, n_blocks)
         self.ref = ctypes.byref(self.c)
+
+
+# A decode step makes a few of these calls per layer, each a few microseconds on
+# the GPU, so the checks take the short way when all is well and find out what
+# is wrong only when something is.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 
 
 def _kv8_ptr(cache, t, dtype, shape, what):
     """Address of a dense tensor of a kv8 call, on the cache's device."""
     if t is None:
         return None
+    if t.dtype is dtype and t.shape == shape and t.get_device() == cache.index and t.is_contiguous():
+        return t.data_ptr()
     if t.dtype != dtype or tuple(t.shape) != shape:
         raise ValueError("%s is %s %s; got %s %s" % (what, dtype, shape, t.dtype, tuple(t.shape)))
     if t.device != cache.device:
         raise ValueError("%s is on %s, the cache on %s" % (what, t.device, cache.device))
-    if not t.is_contiguous():
-        raise ValueError("%s must be contiguous" % what)
-    return t.data_ptr()
+    raise ValueError("%s must be contiguous" % what)
 
 
 def _kv8_rows(cache, t, heads, what):
     """Address and (batch, row) strides of rows [batch, T, heads, head_dim]
     whose heads and channels are dense (a slice of a wider row is fine)."""
-    if t.dim() != 4 or t.shape[0] != cache.batch or t.shape[2] != heads or t.shape[3] != cache.head_dim:
-        raise ValueError("%s is [%d, T, %s, %d]; got %s"
-                         % (what, cache.batch, heads, cache.head_dim, tuple(t.shape)))
-    if t.device != cache.device:
+    shape, dim = t.shape, cache.head_dim
+    if len(shape) != 4 or shape[0] != cache.batch or shape[2] != heads or shape[3] != dim:
+        raise ValueError("%s is [%d, T, %s, %d]; got %s" % (what, cache.batch, heads, dim, tuple(shape)))
+    if t.get_device() != cache.index:
         raise ValueError("%s is on %s, the cache on %s" % (what, t.device, cache.device))
+    T = shape[1]
+    if t.is_contiguous():
+        return t.data_ptr(), T * heads * dim, heads * dim
     sb, st, sh, sd = t.stride()
-    if (sd != 1 and t.shape[3] > 1) or (sh != t.shape[3] and heads > 1):
+    if sd != 1 or (sh != dim and heads > 1):
         raise ValueError("%s: heads and channels must be dense" % what)
-    T = t.shape[1]
     st = st if T > 1 else 8
-    sb = sb if t.shape[0] > 1 else 8
+    sb = sb if shape[0] > 1 else 8
     if st % 8 or sb % 8:
         raise ValueError("%s: row strides must be multiples of 8 elements" % what)
     return t.data_ptr(), sb, st
 
 
-def _kv8_stream(cache, stream):
-    s = stream if stream is not None else torch.cuda.current_stream(cache.device)
-    return s.cuda_stream
+def _kv8_ws(cache, ws):
+    if ws is None:
+        return None
+    if ws.get_device() != cache.index or not ws.is_contiguous():
+        raise ValueError("the workspace is a contiguous tensor on the cache's device")
+    return ws.data_ptr()
 
 
-class _kv8_device:
-    """Launches go to the cache's device, whichever is current."""
-
-    def __new__(cls, cache):
-        i = cache.device.index
-        if i is None or torch.cuda.current_device() == i:
-            return _SAME_DEVICE
-        return torch.cuda.device(i)
-
-
-class _SameDevice:
-    def __enter__(self):
-        return self
-
-    def __exit__(self, *a):
-        return False
-
-
-_SAME_DEVICE = _SameDevice()
+def _kv8_call(cache, stream, what, fn, *args):
+    """fn(*args, stream) on the cache's device, whichever is current."""
+    if stream is not None:
+        s = stream.cuda_stream
+    else:
+        s = _raw_stream(cache.index) if _raw_stream else torch.cuda.current_stream(cache.device).cuda_stream
+    if _current_device() == cache.index:
+        rc = fn(cache.ref, *args, s)
+    else:
+        with torch.cuda.device(cache.index):
+            rc = fn(cache.ref, *args, s)
+    if rc:
+        raise CSA2Error(rc, what)
 
 
 def kv8_workspace_bytes(cache, T, H, n_sel=0):
@@ -605,55 +611,52 @@ def kv8_workspace_bytes(cache, T, H, n_sel=0):
     return n
 
 
-def _kv8_ws(cache, ws):
-    if ws is None:
-        return None
-    if ws.device != cache.device or not ws.is_contiguous():
-        raise ValueError("the workspace is a contiguous tensor on the cache's device")
-    return ws.data_ptr()
-
-
 def kv8_append(cache, k_new, v_new, start_pos, n_new=None, ws=None, stream=None):
     """k_new, v_new [B, T, n_kv_heads, head_dim] bf16 / fp16 / fp32 (equal
     strides, heads and channels dense) quantised into positions start_pos[b] +
     j, j < n_new[b] (None: T); start_pos, n_new int32 [B].  seq_lens stays."""
-    B = cache.batch
-    if k_new.dtype not in _KV8_DTYPES or v_new.dtype != k_new.dtype or v_new.shape != k_new.shape:
+    dt, B = _KV8_DTYPES.get(k_new.dtype), (cache.batch,)
+    if dt is None or v_new.dtype is not k_new.dtype or v_new.shape != k_new.shape:
         raise ValueError("k_new and v_new are bf16, fp16 or fp32 tensors of one shape and type")
     kp, sb, st = _kv8_rows(cache, k_new, cache.n_kv_heads, "k_new")
     vp, vsb, vst = _kv8_rows(cache, v_new, cache.n_kv_heads, "v_new")
-    if (sb, st) != (vsb, vst):
+    if sb != vsb or st != vst:
         raise ValueError("k_new and v_new must have equal strides")
-    i32 = torch.int32
-    with _kv8_device(cache):
-        _check(lib().csa2_kv8_append(cache.ref, kp, vp, _KV8_DTYPES[k_new.dtype], sb, st, k_new.shape[1],
-                                     _kv8_ptr(cache, start_pos, i32, (B,), "start_pos"),
-                                     _kv8_ptr(cache, n_new, i32, (B,), "n_new"), _kv8_ws(cache, ws),
-                                     _kv8_stream(cache, stream)), "kv8_append")
+    _kv8_call(cache, stream, "kv8_append", lib().csa2_kv8_append, kp, vp, dt, sb, st, k_new.shape[1],
+              _kv8_ptr(cache, start_pos, torch.int32, B, "start_pos"), _kv8_ptr(cache, n_new, torch.int32, B, "n_new"),
+              _kv8_ws(cache, ws))
 
 
 def kv8_read(cache, start_pos, k_out, v_out, n_rows=None, ws=None, stream=None):
     """Positions start_pos[b] + j, j < n_rows[b] (None: T), as values into
     k_out, v_out [B, T, n_kv_heads, head_dim] bf16 / fp16 / fp32."""
-    B, i32 = cache.batch, torch.int32
-    if k_out.dtype not in _KV8_DTYPES or k_out.dim() != 4:
+    dt, B = _KV8_DTYPES.get(k_out.dtype), (cache.batch,)
+    if dt is None or k_out.dim() != 4:
         raise ValueError("k_out and v_out are bf16, fp16 or fp32 [batch, T, n_kv_heads, head_dim]")
-    shape = (B, k_out.shape[1], cache.n_kv_heads, cache.head_dim)
-    with _kv8_device(cache):
-        _check(lib().csa2_kv8_read(cache.ref, _kv8_ptr(cache, start_pos, i32, (B,), "start_pos"),
-                                   _kv8_ptr(cache, n_rows, i32, (B,), "n_rows"), shape[1],
-                                   _kv8_ptr(cache, k_out, k_out.dtype, shape, "k_out"),
-                                   _kv8_ptr(cache, v_out, k_out.dtype, shape, "v_out"), _KV8_DTYPES[k_out.dtype],
-                                   _kv8_ws(cache, ws), _kv8_stream(cache, stream)), "kv8_read")
+    shape = (cache.batch, k_out.shape[1], cache.n_kv_heads, cache.head_dim)
+    _kv8_call(cache, stream, "kv8_read", lib().csa2_kv8_read,
+              _kv8_ptr(cache, start_pos, torch.int32, B, "start_pos"),
+              _kv8_ptr(cache, n_rows, torch.int32, B, "n_rows"), shape[1],
+              _kv8_ptr(cache, k_out, k_out.dtype, shape, "k_out"), _kv8_ptr(cache, v_out, k_out.dtype, shape, "v_out"),
+              dt, _kv8_ws(cache, ws))
 
 
-def _kv8_query(cache, q):
-    if q.dtype not in (torch.bfloat16, torch.float16):
+def _kv8_query(cache, q, n_q):
+    """The query arguments of a call: address, type, strides, T, H, n_q."""
+    dt = _KV8_DTYPES.get(q.dtype)
+    if dt is None or dt == F32:
         raise ValueError("q is bf16 or fp16; got %s" % q.dtype)
     if q.dim() != 4:
         raise ValueError("q is [batch, T, H, head_dim]")
-    qp, sb, st = _kv8_rows(cache, q, q.shape[2], "q")
-    return qp, _KV8_DTYPES[q.dtype], sb, st, q.shape[1], q.shape[2]
+    _, T, H, _ = q.shape
+    qp, sb, st = _kv8_rows(cache, q, H, "q")
+    return qp, dt, sb, st, T, H, _kv8_ptr(cache, n_q, torch.int32, (cache.batch,), "n_q")
+
+
+def _kv8_outputs(cache, q, out, lse, ws):
+    B, T, H, D = q.shape
+    return (_kv8_ptr(cache, out, q.dtype, (B, T, H, D), "out"), _kv8_ptr(cache, lse, torch.float32, (B, T, H), "lse"),
+            _kv8_ws(cache, ws), ws.numel() * ws.element_size())
 
 
 def kv8_attn(cache, q, out, ws, lse=None, window=0, n_q=None, sm_scale=0.0, stream=None):
@@ -661,40 +664,27 @@ def kv8_attn(cache, q, out, ws, lse=None, window=0, n_q=None, sm_scale=0.0, stre
     sequence b at seq_lens[b] - n_q[b] + j; n_q None: T) over the cache into
     out (q's shape and type) and lse fp32 [B, T, H].  window > 0: the last
     `window` positions only."""
-    qp, dt, sb, st, T, H = _kv8_query(cache, q)
-    B = cache.batch
-    with _kv8_device(cache):
-        _check(lib().csa2_kv8_attn(cache.ref, qp, dt, sb, st, T, H, _kv8_ptr(cache, n_q, torch.int32, (B,), "n_q"),
-                                   window, sm_scale, _kv8_ptr(cache, out, q.dtype, (B, T, H, cache.head_dim), "out"),
-                                   _kv8_ptr(cache, lse, torch.float32, (B, T, H), "lse"), _kv8_ws(cache, ws),
-                                   ws.numel() * ws.element_size(), _kv8_stream(cache, stream)), "kv8_attn")
+    _kv8_call(cache, stream, "kv8_attn", lib().csa2_kv8_attn, *_kv8_query(cache, q, n_q), window, sm_scale,
+              *_kv8_outputs(cache, q, out, lse, ws))
 
 
 def kv8_select_blocks(cache, q, block_idx, ws, n_first=0, n_recent=1, n_q=None, stream=None):
     """The blocks every query row's key heads attend to, by the key bounds:
     block_idx int32 [B, T, n_kv_heads, n_sel], ascending, -1 last; the first
     n_first and the newest n_recent visible blocks are always among them."""
-    qp, dt, sb, st, T, H = _kv8_query(cache, q)
-    B, n_sel = cache.batch, block_idx.shape[-1]
-    with _kv8_device(cache):
-        _check(lib().csa2_kv8_select_blocks(
-            cache.ref, qp, dt, sb, st, T, H, _kv8_ptr(cache, n_q, torch.int32, (B,), "n_q"), n_sel, n_first, n_recent,
-            _kv8_ptr(cache, block_idx, torch.int32, (B, T, cache.n_kv_heads, n_sel), "block_idx"), _kv8_ws(cache, ws),
-            ws.numel() * ws.element_size(), _kv8_stream(cache, stream)), "kv8_select_blocks")
+    args, n_sel = _kv8_query(cache, q, n_q), block_idx.shape[-1]
+    _kv8_call(cache, stream, "kv8_select_blocks", lib().csa2_kv8_select_blocks, *args, n_sel, n_first, n_recent,
+              _kv8_ptr(cache, block_idx, torch.int32, (cache.batch, args[4], cache.n_kv_heads, n_sel), "block_idx"),
+              _kv8_ws(cache, ws), ws.numel() * ws.element_size())
 
 
 def kv8_block_attn(cache, q, block_idx, out, ws, lse=None, n_q=None, sm_scale=0.0, stream=None):
     """kv8_attn over the listed blocks alone (block_idx as kv8_select_blocks
     writes it)."""
-    qp, dt, sb, st, T, H = _kv8_query(cache, q)
-    B, n_sel = cache.batch, block_idx.shape[-1]
-    with _kv8_device(cache):
-        _check(lib().csa2_kv8_block_attn(
-            cache.ref, qp, dt, sb, st, T, H, _kv8_ptr(cache, n_q, torch.int32, (B,), "n_q"),
-            _kv8_ptr(cache, block_idx, torch.int32, (B, T, cache.n_kv_heads, n_sel), "block_idx"), n_sel, sm_scale,
-            _kv8_ptr(cache, out, q.dtype, (B, T, H, cache.head_dim), "out"),
-            _kv8_ptr(cache, lse, torch.float32, (B, T, H), "lse"), _kv8_ws(cache, ws),
-            ws.numel() * ws.element_size(), _kv8_stream(cache, stream)), "kv8_block_attn")
+    args, n_sel = _kv8_query(cache, q, n_q), block_idx.shape[-1]
+    _kv8_call(cache, stream, "kv8_block_attn", lib().csa2_kv8_block_attn, *args,
+              _kv8_ptr(cache, block_idx, torch.int32, (cache.batch, args[4], cache.n_kv_heads, n_sel), "block_idx"),
+              n_sel, sm_scale, *_kv8_outputs(cache, q, out, lse, ws))
 
 
 def debug_encode(x, codes, fmt, stream=None):

@@ -142,7 +142,7 @@ def test_binding_refuses_what_would_be_misread(lib):
 
 class _Cache:
     """What the binding's argument checks read of a cache, on the host."""
-    batch, n_kv_heads, head_dim, device = 2, 2, 64, torch.device("cpu")
+    batch, n_kv_heads, head_dim, device, index = 2, 2, 64, torch.device("cpu"), -1
 
 
 def test_binding_row_checks():
@@ -159,7 +159,7 @@ def test_binding_row_checks():
     for bad in (torch.zeros(2, 3), torch.zeros(2, 2, dtype=torch.int64), torch.zeros(4, 2, dtype=torch.float32)[::2]):
         with pytest.raises(ValueError):
             csa2._kv8_ptr(c, bad, torch.float32, (2, 2), "x")
-    c.device = torch.device("meta")
+    c.device, c.index = torch.device("cuda:1"), 1
     with pytest.raises(ValueError):                                      # another device than the cache's
         csa2._kv8_ptr(c, torch.zeros(2, 2), torch.float32, (2, 2), "x")
     with pytest.raises(ValueError):
