@@ -12,7 +12,7 @@ namespace {
 
 constexpr int64_t kMaxRows = (int64_t)1 << 31;
 constexpr int kMostSel = 2048;
-constexpr int64_t kMostScoreBlocks = (int64_t)65535 * 256;  // the score grid's second axis
+constexpr int kMostScoreBlocks = 1 << 20;  // the selection's map of chosen blocks in shared memory
 
 bool aligned(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
 

@@ -19,8 +19,7 @@ namespace csa2 {
 namespace {
 
 constexpr int kWarps = 4, kThreads = kWarps * 32;
-constexpr int kTiles = 4;                          // tiles of 16 blocks a warp scores
-constexpr int kCtaBlocks = kWarps * kTiles * 16;
+constexpr int kPerSm = 5;                          // CTAs an SM: 4, 6, 8 are slower (22.4 us; 23.7, 22.7, 24.6 for 32 sequences)
 
 struct Params {
     DevKv8 c;
@@ -31,88 +30,93 @@ struct Params {
     uint32_t* status;
 };
 
-// Eight query rows in operand layout: whole numbers, the negative part against
-// the lower bounds, the positive against the upper.
-// b[half of bounds][chunk][k step][register].
+// Two 16-bit values as floats.
+__device__ __forceinline__ float2 both(uint32_t w, int is_bf16) {
+    if (is_bf16) return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
+    __half2 h;
+    memcpy(&h, &w, 4);
+    return __half22float2(h);
+}
+
+// Eight query heads in operand layout: whole numbers of at most 127 in units of
+// 2^e.  The 2 D bytes of a block's bounds are one k axis, of which lane column
+// c holds bytes 128 x + 32 c .. + 31: for D = 128 the same 32 channels' lower
+// (x = 0) and upper (x = 1) bounds, for D = 64 lower (c < 2) or upper ones.
 template <int D>
 struct QueryRows {
-    static constexpr int kC = D / 64;
-    uint32_t b[2][kC][4][2];
-    float unit[2];   // 2^e of rows 2c and 2c + 1
+    uint32_t b[16];                      // two channels a word
+    float unit[2];                       // 2^e of rows 2c and 2c + 1
 
-    // Two 16-bit values as floats, what is not finite as 0.
-    static __device__ __forceinline__ float2 both(uint32_t w, int is_bf16) {
-        float2 f;
-        if (is_bf16) {
-            f = make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
-        } else {
-            __half2 h;
-            memcpy(&h, &w, 4);
-            f = __half22float2(h);
-        }
-        if (!(fabsf(f.x) <= 3.4028235e38f)) f.x = 0.0f;
-        if (!(fabsf(f.y) <= 3.4028235e38f)) f.y = 0.0f;
-        return f;
-    }
-    static __device__ __forceinline__ uint32_t pack(float x, float y) {
-        const __half2 h = __floats2half2_rn(x, y);
-        uint32_t w;
-        memcpy(&w, &h, 4);
-        return w;
-    }
-    // Heads g0 + r of key head h (lane column c holds chunks c, c + 4).
+    // Heads g0 + r of key head h.
     __device__ __forceinline__ void load(const Params& p, int bq, int j, int h, int g0, int r, int c) {
         const int g = g0 + r;
-        const bool ok = g < p.G;
-        uint32_t raw[kC][8];
         const uint16_t* src = static_cast<const uint16_t*>(p.q.q) + (int64_t)bq * p.q.stride_b +
-                              (int64_t)j * p.q.stride_t + (int64_t)(h * p.G + g) * D;
+                              (int64_t)j * p.q.stride_t + (int64_t)(h * p.G + g) * D + (D == 128 ? c : c & 1) * 32;
 #pragma unroll
-        for (int k = 0; k < kC; ++k) {
-            uint4 x = make_uint4(0, 0, 0, 0), y = x;
-            if (ok) {
-                const uint4* s4 = reinterpret_cast<const uint4*>(src + (c + 4 * k) * 16);
-                x = __ldg(s4);
-                y = __ldg(s4 + 1);
+        for (int i = 0; i < 4; ++i) {
+            uint4 x = make_uint4(0, 0, 0, 0);
+            if (g < p.G) x = __ldg(reinterpret_cast<const uint4*>(src) + i);
+            b[4 * i] = x.x, b[4 * i + 1] = x.y, b[4 * i + 2] = x.z, b[4 * i + 3] = x.w;
+        }
+    }
+    __device__ __forceinline__ void round(const Params& p, int g0, int r, int c) {
+        const uint32_t inf = p.q.is_bf16 ? 0x7F80u : 0x7C00u;
+        uint32_t odd = 0;                // what is not finite counts as 0: rare, out of the way
+#pragma unroll
+        for (int i = 0; i < 16; ++i) odd |= (uint32_t)((b[i] & inf) == inf) | (uint32_t)((b[i] >> 16 & inf) == inf);
+        if (__any_sync(0xFFFFFFFFu, odd)) {
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+                if ((b[i] & inf) == inf) b[i] &= 0xFFFF0000u;
+                if ((b[i] >> 16 & inf) == inf) b[i] &= 0xFFFFu;
             }
-            raw[k][0] = x.x, raw[k][1] = x.y, raw[k][2] = x.z, raw[k][3] = x.w;
-            raw[k][4] = y.x, raw[k][5] = y.y, raw[k][6] = y.z, raw[k][7] = y.w;
         }
         float amax = 0.0f;
 #pragma unroll
-        for (int k = 0; k < kC; ++k)
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const float2 f = both(raw[k][i], p.q.is_bf16);
-                amax = fmaxf(amax, fmaxf(fabsf(f.x), fabsf(f.y)));
-            }
+        for (int i = 0; i < 16; ++i) {
+            const float2 f = both(b[i], p.q.is_bf16);
+            amax = fmaxf(amax, fmaxf(fabsf(f.x), fabsf(f.y)));
+        }
         amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, 1));
         amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, 2));
         // the least e with amax <= 127 * 2^e (127 = 1.984375 * 2^6)
         const uint32_t u = __float_as_uint(amax);
         int e = (int)(u >> 23) - 127 - 6 + ((u & 0x7FFFFFu) > 0x7E0000u ? 1 : 0);
         e = e < -118 ? -118 : e;
-        const float mine = ok ? exp2_int(e) : -INFINITY, down = exp2_int(-e);
+        const float mine = g0 + r < p.G ? exp2_int(e) : -INFINITY, down = exp2_int(-e);
         unit[0] = __shfl_sync(0xFFFFFFFFu, mine, 2 * c * 4);
         unit[1] = __shfl_sync(0xFFFFFFFFu, mine, (2 * c + 1) * 4);
+        constexpr float kWhole = 12582912.0f;   // 1.5 * 2^23: adding it rounds to whole numbers, ties to even
 #pragma unroll
-        for (int k = 0; k < kC; ++k)
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {   // word i: channels 2i, 2i + 1 of the chunk, k step i / 2
-                const float2 f = both(raw[k][i], p.q.is_bf16);
-                const float x = rintf(f.x * down), y = rintf(f.y * down);
-                b[0][k][i >> 1][i & 1] = pack(fminf(x, 0.0f), fminf(y, 0.0f));
-                b[1][k][i >> 1][i & 1] = pack(fmaxf(x, 0.0f), fmaxf(y, 0.0f));
+        for (int i = 0; i < 16; ++i) {
+            const float2 f = both(b[i], p.q.is_bf16);
+            __half2 h = __floats2half2_rn(__fmaf_rn(f.x, down, kWhole) - kWhole, __fmaf_rn(f.y, down, kWhole) - kWhole);
+            if (D == 64) {   // this lane's half of the k axis is all lower or all upper bounds
+                const __half2 z = __floats2half2_rn(0.0f, 0.0f);
+                h = c < 2 ? __hmin2(h, z) : __hmax2(h, z);
             }
+            memcpy(&b[i], &h, 4);
+        }
+    }
+    // Word w as it meets the lower (x = 0) or upper bounds.
+    __device__ __forceinline__ uint32_t part(int x, int w) const {
+        if (D == 64) return b[w];
+        uint32_t lo, hi;
+        asm("min.f16x2 %0, %1, %2;" : "=r"(lo) : "r"(b[w]), "r"(0u));
+        asm("max.f16x2 %0, %1, %2;" : "=r"(hi) : "r"(b[w]), "r"(0u));
+        return x ? hi : lo;
     }
 };
 
-// The row of a CTA: sequence b, token j, key head h; false beyond the call's rows.
-__device__ __forceinline__ bool row_of(const Params& p, int row, int& b, int& j, int& h, int& visible, bool report) {
-    h = row % p.c.heads;
-    const int bj = row / p.c.heads;
-    b = bj / p.q.T;
-    j = bj - b * p.q.T;
+// 32 bytes, so that the four lanes of a block's row ask for whole 128-byte lines.
+__device__ __forceinline__ void load32(uint32_t (&w)[8], const uint8_t* p) {
+    asm volatile("ld.global.nc.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                 : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]), "=r"(w[4]), "=r"(w[5]), "=r"(w[6]), "=r"(w[7])
+                 : "l"(p));
+}
+
+// Blocks that query row (b, j) sees; false beyond the call's rows.
+__device__ __forceinline__ bool row_of(const Params& p, int b, int j, int& visible, bool report) {
     uint32_t* status = report ? p.status : nullptr;
     const int L = kv8_len(p.c, b, status), n = kv8_rows(p.q.n_q, b, p.q.T, status);
     const int pos = L - n + j;
@@ -120,117 +124,175 @@ __device__ __forceinline__ bool row_of(const Params& p, int row, int& b, int& j,
     return j < n;
 }
 
-// Scores of kCtaBlocks blocks of one row: a warp takes four tiles of 16 blocks
-// (the rows of the matrix tile; the query heads are its 8 columns), 2 D bytes a
-// block straight from global memory into operand registers (four lanes read 64
-// adjacent bytes of a block at a time), the next tile's loads in flight while
-// one is multiplied.
+// Scores of all rows.  The tiles of 16 blocks of every row (token, key head) of
+// every sequence form one line that the grid's warps cut into equal runs (the
+// lengths are on the device: every warp sums them itself), since rows of one
+// batch differ in length and a warp has only a few tiles.  A tile's blocks are the
+// rows of the matrix tile, eight query heads its columns; the 2 D bytes a block
+// come straight from global memory into operand registers, 32 bytes a lane: the
+// four lanes of a block take a whole line, since an SM asks for about 340 lines
+// a microsecond, whatever part of a line it asks for.  The next line's bounds
+// are in flight while one is multiplied, and the loop is short: fetching
+// straight-line code cost more than the data.
 template <int D>
-__global__ void __launch_bounds__(kThreads, 4) k_kv8_score(const __grid_constant__ Params p) {
-    constexpr int kC = D / 64;
+__global__ void __launch_bounds__(kThreads, kPerSm) k_kv8_score(const __grid_constant__ Params p) {
+    constexpr int kLines = D / 64;
     pdl_begin();
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, r = lane >> 2, c = lane & 3;
-    int b, j, h, visible;
-    if (!row_of(p, blockIdx.x, b, j, h, visible, blockIdx.y == 0 && threadIdx.x == 0)) return;
-    const int first = (blockIdx.y * kWarps + warp) * kTiles * 16;
-    if (first >= visible) return;
-    int unit[kTiles][2];   // physical block * heads + head of blocks r and r + 8 of every tile, -1: none
-#pragma unroll
-    for (int i = 0; i < kTiles; ++i)
-#pragma unroll
-        for (int half = 0; half < 2; ++half) {
-            const int lb = first + i * 16 + half * 8 + r;
-            unit[i][half] = lb < visible ? kv8_block(p.c, b, lb) : -2;
-        }
-#pragma unroll
-    for (int i = 0; i < kTiles; ++i)
-#pragma unroll
-        for (int half = 0; half < 2; ++half) {
-            if (unit[i][half] == -1 && c == 0) flag(p.status, kStatusBounds);
-            if (unit[i][half] >= 0) unit[i][half] = unit[i][half] * p.c.heads + h;
-        }
-    auto load = [&](uint4 (&w)[2][2][kC], const int (&u)[2]) {
-#pragma unroll
-        for (int half = 0; half < 2; ++half)
-#pragma unroll
-            for (int m = 0; m < 2; ++m)
-#pragma unroll
-                for (int k = 0; k < kC; ++k) {
-                    w[half][m][k] = make_uint4(0, 0, 0, 0);
-                    if (u[half] >= 0)
-                        w[half][m][k] = __ldg(reinterpret_cast<const uint4*>(p.c.k_bounds + (int64_t)u[half] * 2 * D + m * D) + c + 4 * k);
-                }
+    const int lane = threadIdx.x & 31, r = lane >> 2, c = lane & 3;
+    const int nb = p.c.batch, per = (nb + 31) >> 5, heads = p.c.heads;
+    struct Seq {
+        int L, n, tiles;      // positions, query rows, tiles that its last row sees
     };
-    float best[kTiles][2];   // blocks r and r + 8 of every tile
+    auto sequence = [&](int b, uint32_t* status) {
+        Seq q = {0, 0, 0};
+        if (b < nb) {
+            q.L = kv8_len(p.c, b, status);
+            q.n = kv8_rows(p.q.n_q, b, p.q.T, status);
+            if (q.L > 0) q.tiles = ((q.L - 1) >> (p.c.bs_log2 + 4)) + 1;
+        }
+        return q;
+    };
+    uint32_t* report = blockIdx.x == 0 && threadIdx.x < 32 ? p.status : nullptr;
+    Seq mine = {0, 0, 0};
+    int64_t sum = 0;
+    for (int i = 0; i < per; ++i) {
+        mine = sequence(lane * per + i, report);
+        sum += (int64_t)mine.n * heads * mine.tiles;
+    }
+    int64_t upto = sum;
 #pragma unroll
-    for (int i = 0; i < kTiles; ++i) best[i][0] = best[i][1] = -INFINITY;
-    for (int g0 = 0; g0 < p.G; g0 += 8) {
-        uint4 w[2][2][2][kC];
-        load(w[0], unit[0]);
-        QueryRows<D> q;
-        q.load(p, b, j, h, g0, r, c);
-#pragma unroll
-        for (int i = 0; i < kTiles; ++i) {
-            if (i + 1 < kTiles) load(w[(i + 1) & 1], unit[i + 1]);
-            float acc[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-            for (int m = 0; m < 2; ++m)
-#pragma unroll
-                for (int k = 0; k < kC; ++k) {
-                    const uint4 &x = w[i & 1][0][m][k], &y = w[i & 1][1][m][k];
-                    const uint32_t xs[4] = {x.x, x.y, x.z, x.w}, ys[4] = {y.x, y.y, y.z, y.w};
-#pragma unroll
-                    for (int s = 0; s < 4; ++s) {
-                        const uint32_t a[4] = {half2_lo(xs[s]), half2_lo(ys[s]), half2_hi(xs[s]), half2_hi(ys[s])};
-                        mma_16816(acc, a, q.b[m][k][s][0], q.b[m][k][s][1]);
-                    }
-                }
-            // rows without a query head hold 0 * -inf: fmaxf drops the NaN
-            best[i][0] = fmaxf(best[i][0], fmaxf(acc[0] * q.unit[0], acc[1] * q.unit[1]));
-            best[i][1] = fmaxf(best[i][1], fmaxf(acc[2] * q.unit[0], acc[3] * q.unit[1]));
+    for (int o = 1; o < 32; o <<= 1) {
+        const int64_t v = __shfl_up_sync(0xFFFFFFFFu, upto, o);
+        if (lane >= o) upto += v;
+    }
+    const int64_t before = upto - sum, total = __shfl_sync(0xFFFFFFFFu, upto, 31);
+    const int warps = gridDim.x * kWarps, id = blockIdx.x * kWarps + (threadIdx.x >> 5);
+    const int share = total < warps ? (int)total : warps;
+    if (id >= share) return;
+    const int64_t size = total / share, more = total - size * share;
+    int64_t u = size * id + (id < more ? id : more);
+    const int64_t u1 = u + size + (id < more ? 1 : 0);
+    // the sequence, row and tile of step u
+    const int at = 31 - __clz(__ballot_sync(0xFFFFFFFFu, before <= u));
+    int64_t off = u - __shfl_sync(0xFFFFFFFFu, before, at);
+    int b = at * per;
+    Seq seq;
+    if (per == 1) {
+        seq.L = __shfl_sync(0xFFFFFFFFu, mine.L, at);
+        seq.n = __shfl_sync(0xFFFFFFFFu, mine.n, at);
+        seq.tiles = __shfl_sync(0xFFFFFFFFu, mine.tiles, at);
+    } else {
+        for (;; ++b) {
+            seq = sequence(b, nullptr);
+            const int64_t t = (int64_t)seq.n * heads * seq.tiles;
+            if (off < t) break;
+            off -= t;
         }
     }
-    float* out = p.scores + (int64_t)blockIdx.x * p.c.max_blocks;
+    int row = (int)(off / seq.tiles), t0 = (int)(off - (int64_t)row * seq.tiles);
+
+    while (u < u1) {
+        const int j = row / heads, h = row - j * heads;
+        const int nt = seq.tiles - t0 < u1 - u ? seq.tiles - t0 : (int)(u1 - u), first = t0 * 16;
+        const int pos = seq.L - seq.n + j, visible = pos < 0 ? 0 : (pos >> p.c.bs_log2) + 1;
+        auto page = [&](int t, int half) {      // physical block of block r (+ 8) of tile t
+            const int lb = first + t * 16 + half * 8 + r;
+            return t < nt && lb < visible ? kv8_block(p.c, b, lb) : -1;
+        };
+        auto load = [&](uint32_t (&w)[2][8], const int (&phys)[2], int x) {
 #pragma unroll
-    for (int i = 0; i < kTiles; ++i)
+            for (int half = 0; half < 2; ++half) {
 #pragma unroll
-        for (int half = 0; half < 2; ++half) {
-            float v = best[i][half];
-            v = fmaxf(v, __shfl_xor_sync(0xFFFFFFFFu, v, 1));
-            v = fmaxf(v, __shfl_xor_sync(0xFFFFFFFFu, v, 2));
-            const int lb = first + i * 16 + half * 8 + r;
-            if (c == 0 && lb < visible)
-                out[lb] = unit[i][half] < 0 ? -INFINITY : v * __ldg(p.c.k_scale + unit[i][half]);
+                for (int i = 0; i < 8; ++i) w[half][i] = 0;
+                if (phys[half] >= 0)
+                    load32(w[half], p.c.k_bounds + ((int64_t)phys[half] * heads + h) * 2 * D + x * 128 + c * 32);
+            }
+        };
+        float* out = p.scores + ((int64_t)(b * p.q.T + j) * heads + h) * p.c.max_blocks;
+        for (int g0 = 0; g0 < p.G && first < visible; g0 += 8) {
+            int here[2] = {page(0, 0), page(0, 1)}, next[2] = {page(1, 0), page(1, 1)};
+            QueryRows<D> q;
+            q.load(p, b, j, h, g0, r, c);
+            uint32_t w[2][8], v[2][8];
+            load(w, here, 0);
+            q.round(p, g0, r, c);
+            float acc[4] = {0.0f, 0.0f, 0.0f, 0.0f}, ks[2];
+            int t = 0, x = 0;
+#pragma unroll 1
+            for (;;) {
+                const bool last = x == kLines - 1;      // of the tile
+                load(v, last ? next : here, last ? 0 : 1);
+                if (x == 0) {
+#pragma unroll
+                    for (int half = 0; half < 2; ++half)
+                        ks[half] = here[half] >= 0 ? __ldg(p.c.k_scale + (int64_t)here[half] * heads + h) : 0.0f;
+                }
+#pragma unroll
+                for (int s = 0; s < 8; ++s) {
+                    const uint32_t a[4] = {half2_lo(w[0][s]), half2_lo(w[1][s]), half2_hi(w[0][s]), half2_hi(w[1][s])};
+                    mma_16816(acc, a, q.part(x, 2 * s), q.part(x, 2 * s + 1));
+                }
+                if (last) {
+                    // rows without a query head hold 0 * -inf: fmaxf drops the NaN
+                    float best[2] = {fmaxf(acc[0] * q.unit[0], acc[1] * q.unit[1]), fmaxf(acc[2] * q.unit[0], acc[3] * q.unit[1])};
+#pragma unroll
+                    for (int half = 0; half < 2; ++half) {
+                        best[half] = fmaxf(best[half], __shfl_xor_sync(0xFFFFFFFFu, best[half], 1));
+                        best[half] = fmaxf(best[half], __shfl_xor_sync(0xFFFFFFFFu, best[half], 2));
+                        const int lb = first + t * 16 + half * 8 + r;
+                        if (c == 0 && lb < visible) {
+                            if (here[half] < 0) flag(p.status, kStatusBounds);
+                            const float score = here[half] < 0 ? -INFINITY : best[half] * ks[half];
+                            out[lb] = g0 ? fmaxf(score, out[lb]) : score;
+                        }
+                    }
+                    acc[0] = acc[1] = acc[2] = acc[3] = 0.0f;
+                    ++t;
+                    if (t >= nt || first + t * 16 >= visible) break;
+#pragma unroll
+                    for (int half = 0; half < 2; ++half) {
+                        here[half] = next[half];
+                        next[half] = page(t + 1, half);
+                    }
+                    x = 0;
+                } else {
+                    ++x;
+                }
+#pragma unroll
+                for (int half = 0; half < 2; ++half)
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) w[half][i] = v[half][i];
+            }
         }
+        u += nt;
+        t0 = 0;
+        if (++row >= seq.n * heads) {
+            row = 0;
+            do seq = sequence(++b, nullptr);
+            while (b < nb && seq.n * seq.tiles == 0);
+        }
+    }
 }
 
 // ---------------------------------------------------------------- the best blocks of a row
 constexpr int kSelThreads = 1024;
 constexpr int kBins = 2048;
 constexpr int kCand = 2048;      // candidates resolved by rank
-constexpr int kMostSel = 2048;
 
 struct SelSmem {
     uint32_t hist[kBins];
     uint32_t cand_key[kCand];
     int cand_idx[kCand];
-    int chosen[kMostSel];
-    uint32_t red[kSelThreads / 32][2];
-    uint32_t cut_key;
-    int cut_idx, n_cand, n_chosen, bin, above;
+    uint32_t red[32][2];
+    int n_cand, bin, above;
 };
 
 __device__ __forceinline__ uint32_t block_sum(uint32_t v, SelSmem& s) {
-    const int warp = threadIdx.x >> 5;
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
+    v = __reduce_add_sync(0xFFFFFFFFu, v);
     __syncthreads();
-    if ((threadIdx.x & 31) == 0) s.red[warp][0] = v;
+    if ((threadIdx.x & 31) == 0) s.red[threadIdx.x >> 5][0] = v;
     __syncthreads();
-    uint32_t t = 0;
-#pragma unroll
-    for (int w = 0; w < kSelThreads / 32; ++w) t += s.red[w][0];
-    return t;
+    return __reduce_add_sync(0xFFFFFFFFu, s.red[threadIdx.x & 31][0]);
 }
 
 // One CTA per row.  The blocks that compete are those between the first and
@@ -238,25 +300,35 @@ __device__ __forceinline__ uint32_t block_sum(uint32_t v, SelSmem& s) {
 // the greatest score find the bin with the cut, whose members are ranked
 // exactly by (score, lower index first).  Many equal scores (a bin too full
 // to rank) are cut by bisection over the score's bits and then over the index.
-// The chosen are put in ascending order by counting.  KPT keys a thread stay in
-// registers; KPT == 0: rows of any length, keys kept in the scores' place.
+// The chosen are bits of a map over the row's blocks, read out in order.  KPT
+// keys a thread stay in registers, fetched before the row's length is known;
+// KPT == 0: rows of any length, keys kept in the scores' place.
 template <int KPT>
 __global__ void __launch_bounds__(kSelThreads) k_kv8_select(const __grid_constant__ Params p) {
     __shared__ SelSmem s;
+    extern __shared__ uint32_t map[];                          // a bit a block
     pdl_begin();
-    const int tid = threadIdx.x;
-    int b, j, h, visible;
-    if (!row_of(p, blockIdx.x, b, j, h, visible, false)) return;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    uint32_t* row = reinterpret_cast<uint32_t*>(p.scores + (int64_t)blockIdx.x * p.c.max_blocks);
+    constexpr int kKeys = KPT ? KPT : 1;
+    uint32_t reg[kKeys];
+    if (KPT) {
+#pragma unroll
+        for (int i = 0; i < kKeys; ++i) {
+            const int at = i * kSelThreads + tid;
+            reg[i] = at < p.c.max_blocks ? row[at] : 0u;
+        }
+    }
+    const int bj = blockIdx.x / p.c.heads, b = bj / p.q.T;
+    int visible;
+    if (!row_of(p, b, bj - b * p.q.T, visible, false)) return;
     int32_t* out = p.idx + (int64_t)blockIdx.x * p.n_sel;
-    const int k = p.n_sel < visible ? p.n_sel : visible;
     if (visible <= p.n_sel) {
-        for (int i = tid; i < p.n_sel; i += kSelThreads) out[i] = i < k ? i : -1;
+        for (int i = tid; i < p.n_sel; i += kSelThreads) out[i] = i < visible ? i : -1;
         return;
     }
     const int c0 = p.n_first, c1 = visible - p.n_recent;       // competing blocks [c0, c1); c0 <= c1 as n_sel < visible
-    const int want = k - p.n_first - p.n_recent;
-    uint32_t* row = reinterpret_cast<uint32_t*>(p.scores + (int64_t)blockIdx.x * p.c.max_blocks);
-    uint32_t reg[KPT ? KPT : 1];
+    const int want = p.n_sel - p.n_first - p.n_recent, words = (visible + 31) >> 5;
     auto key_of = [](uint32_t bits) {
         const float f = __uint_as_float(bits);
         return isnan(f) ? 0u : ordered_key(f);
@@ -265,24 +337,20 @@ __global__ void __launch_bounds__(kSelThreads) k_kv8_select(const __grid_constan
     auto each = [&](auto&& f) {
         if (KPT) {
 #pragma unroll
-            for (int i = 0; i < (KPT ? KPT : 1); ++i) {
-                const int at = c0 + i * kSelThreads + tid;
-                if (at < c1) f(at, reg[i]);
+            for (int i = 0; i < kKeys; ++i) {
+                const int at = i * kSelThreads + tid;
+                if (at >= c0 && at < c1) f(at, reg[i]);
             }
         } else {
 #pragma unroll 4
             for (int at = c0 + tid; at < c1; at += kSelThreads) f(at, row[at]);
         }
     };
+    auto choose = [&](int at) { atomicOr(map + (at >> 5), 1u << (at & 31)); };
     uint32_t lo = 0xFFFFFFFFu, hi = 0;
     if (KPT) {
 #pragma unroll
-        for (int i = 0; i < (KPT ? KPT : 1); ++i) {
-            const int at = c0 + i * kSelThreads + tid;
-            reg[i] = at < c1 ? row[at] : 0u;
-        }
-#pragma unroll
-        for (int i = 0; i < (KPT ? KPT : 1); ++i) reg[i] = key_of(reg[i]);
+        for (int i = 0; i < kKeys; ++i) reg[i] = key_of(reg[i]);
     } else {
         for (int at = c0 + tid; at < c1; at += kSelThreads) row[at] = key_of(row[at]);
     }
@@ -292,19 +360,23 @@ __global__ void __launch_bounds__(kSelThreads) k_kv8_select(const __grid_constan
     });
     lo = __reduce_min_sync(0xFFFFFFFFu, lo);
     hi = __reduce_max_sync(0xFFFFFFFFu, hi);
-    if ((tid & 31) == 0) s.red[tid >> 5][0] = lo, s.red[tid >> 5][1] = hi;
+    if (lane == 0) s.red[warp][0] = lo, s.red[warp][1] = hi;
     for (int i = tid; i < kBins; i += kSelThreads) s.hist[i] = 0;
-    if (tid == 0) s.n_cand = s.n_chosen = 0;
+    for (int i = tid; i < words; i += kSelThreads) {           // the first and the newest are chosen
+        uint32_t m = 0;
+        for (int x = i * 32; x < i * 32 + 32; ++x)
+            if (x < c0 || (x >= c1 && x < visible)) m |= 1u << (x & 31);
+        map[i] = m;
+    }
+    if (tid == 0) s.n_cand = 0;
     __syncthreads();
-    lo = __reduce_min_sync(0xFFFFFFFFu, s.red[tid & 31][0]);   // 32 warps
-    hi = __reduce_max_sync(0xFFFFFFFFu, s.red[tid & 31][1]);
+    lo = __reduce_min_sync(0xFFFFFFFFu, s.red[lane][0]);       // 32 warps
+    hi = __reduce_max_sync(0xFFFFFFFFu, s.red[lane][1]);
     const float flo = lo ? key_score(lo) : -INFINITY, fhi = hi ? key_score(hi) : -INFINITY;
     const float per = (float)(kBins - 1) / (fhi - flo);
     const bool linear = fhi - flo > 0.0f && fhi - flo < INFINITY && per < INFINITY;
-    uint32_t cut_key = 0;      // chosen: key > cut_key, or key == cut_key with index <= cut_idx
-    int cut_idx = -1;
-    bool ranked = false;
-    if (want > 0 && linear) {
+    bool done = want == 0;
+    if (!done && linear) {
         auto bin_of = [&](uint32_t key) {
             const int v = (int)((key_score(key) - flo) * per);
             return v < 0 ? 0 : (v > kBins - 1 ? kBins - 1 : v);
@@ -317,12 +389,12 @@ __global__ void __launch_bounds__(kSelThreads) k_kv8_select(const __grid_constan
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
                 const uint32_t v = __shfl_up_sync(0xFFFFFFFFu, inc, o);
-                if ((tid & 31) >= o) inc += v;
+                if (lane >= o) inc += v;
             }
-            if ((tid & 31) == 31) s.red[tid >> 5][0] = inc;
+            if (lane == 31) s.red[warp][0] = inc;
             __syncthreads();
-            uint32_t w = s.red[tid & 31][0];
-            w = __reduce_add_sync(0xFFFFFFFFu, (tid & 31) < (tid >> 5) ? w : 0u);
+            uint32_t w = s.red[lane][0];
+            w = __reduce_add_sync(0xFFFFFFFFu, lane < warp ? w : 0u);
             const uint32_t after = w + inc, before = after - n;
             if (before < (uint32_t)want && after >= (uint32_t)want) {
                 const bool second = before + n0 < (uint32_t)want;
@@ -331,35 +403,33 @@ __global__ void __launch_bounds__(kSelThreads) k_kv8_select(const __grid_constan
             }
         }
         __syncthreads();
-        const int bin = s.bin, need = want - s.above;
-        const int members = (int)s.hist[bin];
+        const int bin = s.bin, need = want - s.above, members = (int)s.hist[bin];
         if (members <= kCand) {
-            each([&](int at, uint32_t key) {
-                if (bin_of(key) == bin) {
+            each([&](int at, uint32_t key) {     // higher bins are chosen, members of this one ranked
+                const int v = bin_of(key);
+                if (v > bin) choose(at);
+                if (v == bin) {
                     const int i = atomicAdd(&s.n_cand, 1);
                     s.cand_key[i] = key;
                     s.cand_idx[i] = at;
                 }
             });
             __syncthreads();
-            // the need-th best member is the cut: keys of higher bins are greater
-            for (int i = tid; i < members; i += kSelThreads) {
+            for (int i = warp; i < members; i += 32) {          // a warp a member
                 const uint32_t key = s.cand_key[i];
                 const int at = s.cand_idx[i];
                 int rank = 0;
-                for (int o = 0; o < members; ++o) {
+                for (int o = lane; o < members; o += 32) {
                     const uint32_t ko = s.cand_key[o];
                     rank += ko > key || (ko == key && s.cand_idx[o] < at);
                 }
-                if (rank == need - 1) s.cut_key = key, s.cut_idx = at;
+                rank = __reduce_add_sync(0xFFFFFFFFu, rank);
+                if (lane == 0 && rank < need) choose(at);
             }
-            __syncthreads();
-            cut_key = s.cut_key;
-            cut_idx = s.cut_idx;
-            ranked = true;
+            done = true;
         }
     }
-    if (want > 0 && !ranked) {
+    if (!done) {
         // the greatest key with at least `want` keys >= it, then the index of the last tie taken
         uint32_t a = lo, z = hi;
         while (a < z) {
@@ -369,36 +439,43 @@ __global__ void __launch_bounds__(kSelThreads) k_kv8_select(const __grid_constan
             if (block_sum(n, s) >= (uint32_t)want) a = mid;
             else z = mid - 1;
         }
-        cut_key = a;
         uint32_t n = 0;
-        each([&](int, uint32_t key) { n += key > cut_key; });
+        each([&](int, uint32_t key) { n += key > a; });
         const uint32_t need = (uint32_t)want - block_sum(n, s);
         int x = c0, y = c1 - 1;
         while (x < y) {
             const int mid = (x + y) / 2;
             n = 0;
-            each([&](int at, uint32_t key) { n += at <= mid && key == cut_key; });
+            each([&](int at, uint32_t key) { n += at <= mid && key == a; });
             if (block_sum(n, s) >= need) y = mid;
             else x = mid + 1;
         }
-        cut_idx = x;
-    }
-    // the chosen competitors, then all in ascending order
-    if (want > 0)
         each([&](int at, uint32_t key) {
-            if (key > cut_key || (key == cut_key && at <= cut_idx)) {
-                const int i = atomicAdd(&s.n_chosen, 1);
-                if (i < kMostSel) s.chosen[i] = at;
-            }
+            if (key > a || (key == a && at <= x)) choose(at);
         });
+    }
     __syncthreads();
-    for (int i = tid; i < p.n_first; i += kSelThreads) out[i] = i;
-    for (int i = tid; i < p.n_recent; i += kSelThreads) out[p.n_first + want + i] = c1 + i;
-    for (int i = tid; i < want; i += kSelThreads) {
-        const int v = s.chosen[i];
-        int rank = 0;
-        for (int o = 0; o < want; ++o) rank += s.chosen[o] < v;
-        out[p.n_first + rank] = v;
+    // ---- the map in order: kSelThreads words at a time
+    int base = 0;
+    for (int i0 = 0; i0 < words; i0 += kSelThreads) {
+        uint32_t m = i0 + tid < words ? map[i0 + tid] : 0u;
+        const uint32_t n = __popc(m);
+        uint32_t inc = n;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const uint32_t v = __shfl_up_sync(0xFFFFFFFFu, inc, o);
+            if (lane >= o) inc += v;
+        }
+        if (lane == 31) s.red[warp][1] = inc;
+        __syncthreads();
+        const uint32_t w = s.red[lane][1];
+        int at = base + (int)(__reduce_add_sync(0xFFFFFFFFu, lane < warp ? w : 0u) + inc - n);
+        base += (int)__reduce_add_sync(0xFFFFFFFFu, w);
+        for (; m; m &= m - 1) {
+            if (at < p.n_sel) out[at] = (i0 + tid) * 32 + __ffs(m) - 1;
+            ++at;
+        }
+        if (i0 + kSelThreads < words) __syncthreads();
     }
 }
 
@@ -417,14 +494,23 @@ cudaError_t launch_kv8_select(const DevKv8& c, const Kv8Query& q, int n_sel, int
     p.scores = scores;
     p.status = status;
     const unsigned rows = (unsigned)((int64_t)c.batch * q.T * c.heads);
-    const dim3 grid(rows, (c.max_blocks + kCtaBlocks - 1) / kCtaBlocks);
-    cudaError_t e = c.dim == 64 ? launch_pdl(k_kv8_score<64>, grid, kThreads, 0, st, p)
-                                : launch_pdl(k_kv8_score<128>, grid, kThreads, 0, st, p);
+    int dev = 0, sms = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
     if (e != cudaSuccess) return e;
-    if (c.max_blocks <= 2 * kSelThreads) return launch_pdl(k_kv8_select<2>, dim3(rows), kSelThreads, 0, st, p);
-    if (c.max_blocks <= 8 * kSelThreads) return launch_pdl(k_kv8_select<8>, dim3(rows), kSelThreads, 0, st, p);
-    if (c.max_blocks <= 17 * kSelThreads) return launch_pdl(k_kv8_select<17>, dim3(rows), kSelThreads, 0, st, p);
-    return launch_pdl(k_kv8_select<0>, dim3(rows), kSelThreads, 0, st, p);
+    const int64_t most = ((int64_t)rows * ((c.max_blocks + 15) / 16) + kWarps - 1) / kWarps;   // CTAs with a tile a warp
+    const unsigned ctas = (unsigned)(most < sms * kPerSm ? most : sms * kPerSm);
+    e = c.dim == 64 ? launch_pdl(k_kv8_score<64>, ctas, kThreads, 0, st, p)
+                    : launch_pdl(k_kv8_score<128>, ctas, kThreads, 0, st, p);
+    if (e != cudaSuccess) return e;
+    const auto select = c.max_blocks <= 2 * kSelThreads    ? k_kv8_select<2>
+                        : c.max_blocks <= 8 * kSelThreads  ? k_kv8_select<8>
+                        : c.max_blocks <= 17 * kSelThreads ? k_kv8_select<17>
+                                                           : k_kv8_select<0>;
+    const int map_bytes = (c.max_blocks + 31) / 32 * 4;
+    if (map_bytes > 16 * 1024) e = cudaFuncSetAttribute(select, cudaFuncAttributeMaxDynamicSharedMemorySize, map_bytes);
+    if (e != cudaSuccess) return e;
+    return launch_pdl(select, dim3(rows), kSelThreads, map_bytes, st, p);
 }
 
 }  // namespace csa2

@@ -622,7 +622,8 @@ CSA2_API csa2_status csa2_kv8_attn(const csa2_kv8_cache* cache, const void* q, c
  * (-118 <= e; channels that are not finite count as 0): an upper bound of
  * every q . k in the block, up to the rounding of q.  The sums are exact.
  * Bounds cover what the block holds at the time of the call, rows behind p
- * included.  1 <= n_sel <= 2048, n_first + n_recent <= n_sel.
+ * included.  1 <= n_sel <= 2048, n_first + n_recent <= n_sel, max_blocks <=
+ * 2^20.
  */
 CSA2_API csa2_status csa2_kv8_select_blocks(const csa2_kv8_cache* cache, const void* q, csa2_dtype q_dtype,
                                             int64_t stride_b, int64_t stride_t, int T, int H, const int32_t* n_q,
