@@ -10,46 +10,111 @@ namespace {
 
 constexpr int kThreads = 256;
 
-// Eight consecutive channels of a row at the caller's type, as floats.
+// Eight consecutive channels of a row as they come, kW words: what the
+// quantiser needs of them is done on the packed words where it can be.
 template <typename T>
-__device__ __forceinline__ void load8(const T* p, float* x);
+struct Raw;
 
 template <>
-__device__ __forceinline__ void load8<__nv_bfloat16>(const __nv_bfloat16* p, float* x) {
-    const uint4 u = __ldg(reinterpret_cast<const uint4*>(p));
-    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        x[2 * i] = __uint_as_float(w[i] << 16);
-        x[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+struct Raw<float> {
+    static constexpr int kW = 8;
+    static constexpr uint32_t kInf = 0x7F800000u;
+    // the greatest magnitude so far, as an integer: finite < infinite < NaN
+    static __device__ __forceinline__ uint32_t top(uint32_t m, uint32_t w) { return max(m, w & 0x7FFFFFFFu); }
+    static __device__ __forceinline__ uint32_t top(uint32_t m) { return m; }
+    static __device__ __forceinline__ float value(uint32_t top) { return __uint_as_float(top); }
+    static __device__ __forceinline__ uint32_t lower(uint32_t a, uint32_t b) {
+        return __float_as_uint(fminf(__uint_as_float(a), __uint_as_float(b)));
     }
-}
+    static __device__ __forceinline__ uint32_t upper(uint32_t a, uint32_t b) {
+        return __float_as_uint(fmaxf(__uint_as_float(a), __uint_as_float(b)));
+    }
+    static constexpr uint32_t kHighest = 0x7F800000u, kLowest = 0xFF800000u;
+    static __device__ __forceinline__ uint32_t no_nan(uint32_t w) { return (w & 0x7FFFFFFFu) > kInf ? 0u : w; }
+    static __device__ __forceinline__ uint32_t finite(uint32_t w) { return (w & 0x7FFFFFFFu) >= kInf ? 0u : w; }
+    static __device__ __forceinline__ void floats(const uint32_t* w, float* x) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) x[i] = __uint_as_float(w[i]);
+    }
+    static __device__ __forceinline__ float channel(const uint32_t* words, int d) { return __uint_as_float(words[d]); }
+};
+
+// Two 16-bit floats a word.
+template <uint32_t INF>
+struct Raw16 {
+    static constexpr int kW = 4;
+    static constexpr uint32_t kInf = INF;
+    static constexpr uint32_t kHighest = INF * 0x10001u, kLowest = kHighest | 0x80008000u;
+    static __device__ __forceinline__ uint32_t top(uint32_t m, uint32_t w) { return __vmaxu2(m, w & 0x7FFF7FFFu); }
+    static __device__ __forceinline__ uint32_t top(uint32_t m) { return max(m & 0xFFFFu, m >> 16); }
+    static __device__ __forceinline__ uint32_t no_nan(uint32_t w) {
+        if ((w & 0x7FFFu) > INF) w &= 0xFFFF0000u;
+        if ((w >> 16 & 0x7FFFu) > INF) w &= 0xFFFFu;
+        return w;
+    }
+    static __device__ __forceinline__ uint32_t finite(uint32_t w) {
+        if ((w & 0x7FFFu) >= INF) w &= 0xFFFF0000u;
+        if ((w >> 16 & 0x7FFFu) >= INF) w &= 0xFFFFu;
+        return w;
+    }
+};
 
 template <>
-__device__ __forceinline__ void load8<__half>(const __half* p, float* x) {
-    const uint4 u = __ldg(reinterpret_cast<const uint4*>(p));
-    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+struct Raw<__nv_bfloat16> : Raw16<0x7F80u> {
+    static __device__ __forceinline__ float value(uint32_t top) { return __uint_as_float(top << 16); }
+    static __device__ __forceinline__ uint32_t lower(uint32_t a, uint32_t b) {
+        uint32_t r;
+        asm("min.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+        return r;
+    }
+    static __device__ __forceinline__ uint32_t upper(uint32_t a, uint32_t b) {
+        uint32_t r;
+        asm("max.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+        return r;
+    }
+    static __device__ __forceinline__ void floats(const uint32_t* w, float* x) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
+        for (int i = 0; i < 4; ++i) {
+            x[2 * i] = __uint_as_float(w[i] << 16);
+            x[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+        }
+    }
+    static __device__ __forceinline__ float channel(const uint32_t* words, int d) {
+        return __uint_as_float(d & 1 ? words[d >> 1] & 0xFFFF0000u : words[d >> 1] << 16);
+    }
+};
+
+template <>
+struct Raw<__half> : Raw16<0x7C00u> {
+    static __device__ __forceinline__ __half2 half2_of(uint32_t w) {
         __half2 h;
-        memcpy(&h, &w[i], 4);
-        const float2 f = __half22float2(h);
-        x[2 * i] = f.x;
-        x[2 * i + 1] = f.y;
+        memcpy(&h, &w, 4);
+        return h;
     }
-}
-
-template <>
-__device__ __forceinline__ void load8<float>(const float* p, float* x) {
+    static __device__ __forceinline__ float value(uint32_t top) { return __low2float(half2_of(top)); }
+    static __device__ __forceinline__ uint32_t lower(uint32_t a, uint32_t b) {
+        uint32_t r;
+        asm("min.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+        return r;
+    }
+    static __device__ __forceinline__ uint32_t upper(uint32_t a, uint32_t b) {
+        uint32_t r;
+        asm("max.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+        return r;
+    }
+    static __device__ __forceinline__ void floats(const uint32_t* w, float* x) {
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-        const float4 f = __ldg(reinterpret_cast<const float4*>(p) + i);
-        x[4 * i] = f.x;
-        x[4 * i + 1] = f.y;
-        x[4 * i + 2] = f.z;
-        x[4 * i + 3] = f.w;
+        for (int i = 0; i < 4; ++i) {
+            const float2 f = __half22float2(half2_of(w[i]));
+            x[2 * i] = f.x;
+            x[2 * i + 1] = f.y;
+        }
     }
-}
+    static __device__ __forceinline__ float channel(const uint32_t* words, int d) {
+        const float2 f = __half22float2(half2_of(words[d >> 1]));
+        return d & 1 ? f.y : f.x;
+    }
+};
 
 __device__ __forceinline__ void decode8(uint2 codes, float* x) {
     const uint32_t w[2] = {codes.x, codes.y};
@@ -76,16 +141,21 @@ __device__ __forceinline__ uint2 encode8(const float* x) {
 // values: the greatest finite magnitude of those rows gives the scale; a block
 // that already holds rows keeps the larger of its own and the new scale, and
 // when it grows the held codes are rescaled (value * s_old / s_new, exact
-// before its one rounding).  The rows are read once and stay in registers
-// between the two uses; the store is one byte a channel.  Each thread holds
-// eight channels of RPT rows (D / 8 threads a row).
+// before its one rounding).  The rows are read once and stay in registers, as
+// they came, between the two uses; the store is one byte a channel.  Each
+// thread holds eight channels of RPT rows (D / 8 threads a row).  The kernel
+// waits for HBM, so the page table is looked up beside the rows and little is
+// done per element: the greatest magnitude and the least and greatest value of
+// a channel on packed words (the encoder is monotone, so a channel's least
+// code is the code of its least value).
 template <typename T, int D, int RPT>
 __global__ void __launch_bounds__(kThreads) k_kv8_append(DevKv8 c, const T* k_new, const T* v_new, int64_t stride_b,
                                                          int64_t stride_t, const int32_t* start_pos,
                                                          const int32_t* n_new, int n_max, uint32_t* status) {
-    constexpr int kVec = D / 8, kLanes = kThreads / kVec, kWarps = kThreads / 32;
-    __shared__ float s_amax[kWarps];
-    __shared__ float s_lo[kWarps][D], s_hi[kWarps][D];
+    using R = Raw<T>;
+    constexpr int kVec = D / 8, kLanes = kThreads / kVec, kWarps = kThreads / 32, kW = R::kW, kRow = D * kW / 8;
+    __shared__ uint32_t s_top[kWarps];
+    __shared__ uint32_t s_lo[kWarps][kRow], s_hi[kWarps][kRow];
     pdl_begin();
     const int tid = threadIdx.x, b = blockIdx.z, h = blockIdx.y >> 1;
     const bool keys = (blockIdx.y & 1) == 0;
@@ -99,52 +169,65 @@ __global__ void __launch_bounds__(kThreads) k_kv8_append(DevKv8 c, const T* k_ne
     const int64_t end = start + n < cap ? start + n : cap;
     const int64_t lb = (start >> c.bs_log2) + blockIdx.x, pos0 = lb << c.bs_log2;
     if (pos0 >= end) return;
+    const int r0 = start > pos0 ? (int)(start - pos0) : 0;                   // rows already held
+    const int r1 = end - pos0 < bs ? (int)(end - pos0) : bs;                 // rows held after the call
+
+    const int vec = tid % kVec, lane = tid / kVec;
+    const T* src = (keys ? k_new : v_new) + (int64_t)b * stride_b + (int64_t)h * D + vec * 8 + (pos0 - start) * stride_t;
+    uint32_t x[RPT][kW];
+#pragma unroll
+    for (int i = 0; i < RPT; ++i) {
+        const int r = lane + i * kLanes;
+#pragma unroll
+        for (int q = 0; q < kW; q += 4) {
+            uint4 u = make_uint4(0, 0, 0, 0);
+            if (r >= r0 && r < r1) u = __ldg(reinterpret_cast<const uint4*>(src + r * stride_t) + q / 4);
+            x[i][q] = u.x, x[i][q + 1] = u.y, x[i][q + 2] = u.z, x[i][q + 3] = u.w;
+        }
+    }
     const int phys = kv8_block(c, b, (int)lb);
     if (phys < 0) {
         flag(status, kStatusBounds);
         return;
     }
-    const int r0 = start > pos0 ? (int)(start - pos0) : 0;                   // rows already held
-    const int r1 = end - pos0 < bs ? (int)(end - pos0) : bs;                 // rows held after the call
     const int64_t unit = (int64_t)phys * c.heads + h;
     uint8_t* codes = (keys ? c.k : c.v) + unit * bs * D;
     float* scale = (keys ? c.k_scale : c.v_scale) + unit;
     const float s_old = r0 ? *scale : 0.0f;
 
-    const int vec = tid % kVec, lane = tid / kVec;
-    const T* src = (keys ? k_new : v_new) + (int64_t)b * stride_b + (int64_t)h * D + vec * 8;
-    float x[RPT][8];
-    float amax = 0.0f;
-    bool bad = false;
+    // the greatest magnitude of the CTA, as an integer
+    auto greatest = [&]() {
+        uint32_t m = 0;
 #pragma unroll
-    for (int i = 0; i < RPT; ++i) {
-        const int r = lane + i * kLanes;
-        if (r >= r0 && r < r1) load8<T>(src + (pos0 + r - start) * stride_t, x[i]);
-    }
+        for (int i = 0; i < RPT; ++i)
 #pragma unroll
-    for (int i = 0; i < RPT; ++i) {
-        const int r = lane + i * kLanes;
-        if (r >= r0 && r < r1) {
+            for (int q = 0; q < kW; ++q) m = R::top(m, x[i][q]);
+        m = __reduce_max_sync(0xFFFFFFFFu, R::top(m));
+        __syncthreads();
+        if ((tid & 31) == 0) s_top[tid >> 5] = m;
+        __syncthreads();
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                const float a = fabsf(x[i][j]);
-                if (a <= 3.4028235e38f) amax = fmaxf(amax, a);
-                else {
-                    bad = true;                    // infinite: saturates below; NaN: stored as 0
-                    if (isnan(a)) x[i][j] = 0.0f;
-                }
+        for (int w = 0; w < kWarps; ++w) m = max(m, s_top[w]);
+        return m;
+    };
+    uint32_t top = greatest();
+    uint32_t held[RPT][kW];          // (the rows again, where some are not finite: what the scale does not count)
+    if (top >= R::kInf) {            // infinite: saturates below; NaN: stored as 0; neither counts for the scale
+        if (tid == 0) flag(status, kStatusNonFinite);
+#pragma unroll
+        for (int i = 0; i < RPT; ++i)
+#pragma unroll
+            for (int q = 0; q < kW; ++q) {
+                held[i][q] = R::no_nan(x[i][q]);
+                x[i][q] = R::finite(x[i][q]);
             }
-        }
+        top = greatest();
+#pragma unroll
+        for (int i = 0; i < RPT; ++i)
+#pragma unroll
+            for (int q = 0; q < kW; ++q) x[i][q] = held[i][q];
     }
-    if (bad) flag(status, kStatusNonFinite);
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, o));
-    if ((tid & 31) == 0) s_amax[tid >> 5] = amax;
-    __syncthreads();
-#pragma unroll
-    for (int w = 0; w < kWarps; ++w) amax = fmaxf(amax, s_amax[w]);
-    const int e_new = kv8_scale_exp(amax);
-    const float s = fmaxf(exp2_int(e_new), s_old);
+    const float s = fmaxf(exp2_int(kv8_scale_exp(R::value(top))), s_old);
     const float inv = 1.0f / s;                    // exact: a power of two
     if (r0 && s > s_old) {
         const float shrink = s_old * inv;
@@ -157,25 +240,15 @@ __global__ void __launch_bounds__(kThreads) k_kv8_append(DevKv8 c, const T* k_ne
             *p = encode8(y);
         }
     }
-    float lo[8], hi[8];
-#pragma unroll
-    for (int j = 0; j < 8; ++j) lo[j] = 448.0f, hi[j] = -448.0f;
 #pragma unroll
     for (int i = 0; i < RPT; ++i) {
         const int r = lane + i * kLanes;
         if (r >= r0 && r < r1) {
+            float y[8];
+            R::floats(x[i], y);
 #pragma unroll
-            for (int j = 0; j < 8; ++j) x[i][j] *= inv;
-            const uint2 w = encode8(x[i]);
-            *reinterpret_cast<uint2*>(codes + (int64_t)r * D + vec * 8) = w;
-            if (keys) {
-                decode8(w, x[i]);
-#pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    lo[j] = fminf(lo[j], x[i][j]);
-                    hi[j] = fmaxf(hi[j], x[i][j]);
-                }
-            }
+            for (int j = 0; j < 8; ++j) y[j] *= inv;
+            *reinterpret_cast<uint2*>(codes + (int64_t)r * D + vec * 8) = encode8(y);
         }
     }
     if (tid == 0) *scale = s;
@@ -183,27 +256,42 @@ __global__ void __launch_bounds__(kThreads) k_kv8_append(DevKv8 c, const T* k_ne
 
     // the block's bounds in whole units of s: least code rounded down, greatest
     // rounded up, joined with what the held rows had (rescaled outward)
+    uint32_t lo[kW], hi[kW];
+#pragma unroll
+    for (int q = 0; q < kW; ++q) lo[q] = R::kHighest, hi[q] = R::kLowest;
+#pragma unroll
+    for (int i = 0; i < RPT; ++i) {
+        const int r = lane + i * kLanes;
+        if (r >= r0 && r < r1) {
+#pragma unroll
+            for (int q = 0; q < kW; ++q) {
+                lo[q] = R::lower(lo[q], x[i][q]);
+                hi[q] = R::upper(hi[q], x[i][q]);
+            }
+        }
+    }
 #pragma unroll
     for (int o = kVec; o < 32; o <<= 1)
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            lo[j] = fminf(lo[j], __shfl_xor_sync(0xFFFFFFFFu, lo[j], o));
-            hi[j] = fmaxf(hi[j], __shfl_xor_sync(0xFFFFFFFFu, hi[j], o));
+        for (int q = 0; q < kW; ++q) {
+            lo[q] = R::lower(lo[q], __shfl_xor_sync(0xFFFFFFFFu, lo[q], o));
+            hi[q] = R::upper(hi[q], __shfl_xor_sync(0xFFFFFFFFu, hi[q], o));
         }
     if ((tid & 31) < kVec) {
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            s_lo[tid >> 5][vec * 8 + j] = lo[j];
-            s_hi[tid >> 5][vec * 8 + j] = hi[j];
+        for (int q = 0; q < kW; ++q) {
+            s_lo[tid >> 5][vec * kW + q] = lo[q];
+            s_hi[tid >> 5][vec * kW + q] = hi[q];
         }
     }
     __syncthreads();
     if (tid < 2 * D) {
         const int d = tid % D;
         const bool upper = tid >= D;
-        float v = upper ? s_hi[0][d] : s_lo[0][d];
+        float v = upper ? R::channel(s_hi[0], d) : R::channel(s_lo[0], d);
 #pragma unroll
-        for (int w = 1; w < kWarps; ++w) v = upper ? fmaxf(v, s_hi[w][d]) : fminf(v, s_lo[w][d]);
+        for (int w = 1; w < kWarps; ++w) v = upper ? fmaxf(v, R::channel(s_hi[w], d)) : fminf(v, R::channel(s_lo[w], d));
+        v = e4m3_to_float((uint8_t)cvt_e4m3x2(0.0f, v * inv));
         v = upper ? ceilf(v) : floorf(v);
         uint8_t* p = c.k_bounds + unit * 2 * D + tid;
         if (r0) {
