@@ -145,7 +145,7 @@ csa2_status csa2_kv8_read(const csa2_kv8_cache* cache, const int32_t* start_pos,
     CSA2_RANGE("csa2_kv8_read");
     const csa2_status s = check_cache(cache);
     if (s != CSA2_OK) return s;
-    if (!k_out || !v_out || !start_pos || !aligned(k_out, 16) || !aligned(v_out, 16) || !aligned(start_pos, 4) ||
+    if (!k_out || !v_out || !start_pos || !aligned(k_out, 32) || !aligned(v_out, 32) || !aligned(start_pos, 4) ||
         !aligned(n_rows, 4) || !aligned(ws, 16))
         return CSA2_ERR_INVALID_ARG;
     if (dtype != CSA2_BF16 && dtype != CSA2_F16 && dtype != CSA2_F32) return CSA2_ERR_INVALID_ARG;

@@ -588,8 +588,8 @@ CSA2_API csa2_status csa2_kv8_append(const csa2_kv8_cache* cache, const void* k_
 /*
  * Rows back as values: k_out, v_out [batch][T][n_kv_heads][head_dim] (dense, of
  * dtype) <- value(code) * scale of positions start_pos[b] + j, j < n_rows[b],
- * rounded once.  A position outside the cache is written as zeros and sets
- * CSA2_ERR_DEVICE_BOUNDS in ws (nullable).
+ * rounded once; k_out and v_out 32-byte aligned.  A position outside the cache
+ * is written as zeros and sets CSA2_ERR_DEVICE_BOUNDS in ws (nullable).
  */
 CSA2_API csa2_status csa2_kv8_read(const csa2_kv8_cache* cache, const int32_t* start_pos, const int32_t* n_rows,
                                    int T, void* k_out, void* v_out, csa2_dtype dtype, void* ws, void* stream);
