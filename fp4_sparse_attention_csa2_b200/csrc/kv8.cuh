@@ -140,7 +140,7 @@ bool kv8_row_map(CUtensorMap_st* map, const DevKv8& c, void* codes, int box_rows
 // Query rows of a key head (tokens x query heads) up to which the dense
 // attention runs as the streaming kernel (kv8_attn.cu), beyond it as the
 // tensor-core kernel (kv8_prefill.cu).
-constexpr int64_t kKv8StreamRows = 32;
+constexpr int64_t kKv8StreamRows = 16;
 size_t kv8_attn_part_floats(int dim);
 size_t kv8_prefill_part_floats(int dim);
 cudaError_t launch_kv8_attn(const DevKv8& c, const Kv8Attn& a, cudaStream_t st);

@@ -1,7 +1,7 @@
 // Attention over the 8-bit cache for few query rows per sequence (decode and
 // short verification), dense or over listed blocks.
 //
-// One query row needs two products with every cached row, so up to the 32
+// One query row needs two products with every cached row, so up to the 16
 // rows a pass holds the kernel is bound by the codes' bytes (2 * D a position
 // and head) and its work is moving them: the codes go by TMA into a ring of
 // each warp's own (no synchronisation between warps while they stream; the
@@ -17,15 +17,25 @@
 // steps, and of a value row the same channel of two positions is one byte
 // permutation; the weights turn around in registers (movmatrix).
 // tcgen05 would take the codes as they are (kind::f8f6f4) but wants the
-// weights as E4M3 terms and 128 rows a tile; with at most 32 rows it has
+// weights as E4M3 terms and 128 rows a tile; with at most 16 rows it has
 // nothing to win over a kernel that already waits for HBM.
 //
 // Work split: a step is 128 positions of one (sequence, head, row tile); the
 // steps of the whole batch form one line, which the CTAs cut into equal
-// pieces (the lengths are on the device, so every CTA sums them itself).  A
+// pieces (the lengths are on the device, so every warp sums them itself).  A
 // CTA finishes what lies inside its piece; an item that is cut leaves
 // partials (output, running maxima and sum), merged by k_kv8_combine in a
-// fixed order, so results do not vary from run to run.
+// fixed order, so results do not vary from run to run.  (Merges by the CTA
+// that comes last, in the same launch, groups of eight pieces and then the
+// groups, were slower: 17.0 against 12.4 us for 64 blocks of one sequence, 183
+// against 175 us for a million positions; one CTA reads the parts where the
+// second launch reads them with many.)
+//
+// A CTA is four computing warps and one that looks ahead: it walks the line,
+// looks up list entries, pages and scales, and issues the copies into the four
+// warps' rings (a lane a warp).  With that in the computing warps themselves the
+// registers it needs made 16 query rows spill (281 against 158 us for 32
+// sequences of up to 16,384 positions) and its instructions were a third of a tile's.
 #include <cuda.h>
 #include <cuda_fp16.h>
 
@@ -36,7 +46,7 @@
 namespace csa2 {
 namespace {
 
-constexpr int kWarps = 4, kThreads = kWarps * 32;
+constexpr int kWarps = 4, kThreads = (kWarps + 1) * 32;   // computing warps, and the one that looks ahead
 constexpr int kGroup = 16;                // positions of one matrix tile
 constexpr int kTile = 2 * kGroup;         // positions a warp takes at a time
 constexpr int kStep = kWarps * kTile;     // positions a CTA takes at a time
@@ -46,7 +56,10 @@ constexpr float kNone = -3.0e38f;         // running maximum before any position
 // 2^-22 of it keep fp16's full precision.  The 2^8 cancels the 2^-8 of the
 // value codes' bit placement.
 constexpr float kHeadroom = 8.0f;
-constexpr int kMaxCtas = 3 * 148;
+// Two CTAs an SM with three stages a warp (192 KB in flight or in use): three CTAs
+// with two stages take 117 against 112 us for 32 sequences of up to 16,384 tokens.
+constexpr int kPerSm = 2;
+constexpr int kMaxCtas = kPerSm * 148;
 
 struct Params {
     DevKv8 c;
@@ -62,6 +75,11 @@ struct Cursor {
     int b, h, rt, step;
     int steps, tiles, L, n, lo;
 };
+
+// a / b for a >= 0, b > 0: in 32 bits where they fit.
+__device__ __forceinline__ int64_t quotient(int64_t a, int64_t b) {
+    return (a | b) >> 32 ? a / b : (int64_t)((uint32_t)a / (uint32_t)b);
+}
 
 template <int NT, bool LIST>
 struct Work {
@@ -109,9 +127,9 @@ struct Work {
         return (int64_t)p.c.heads * k.tiles * k.steps;
     }
     __device__ __forceinline__ void seek(Cursor& k, int64_t u) const {  // step u of the sequence
-        const int64_t item = u / k.steps;
+        const int64_t item = quotient(u, k.steps);
         k.step = (int)(u - item * k.steps);
-        k.h = (int)(item / k.tiles);
+        k.h = (int)quotient(item, k.tiles);
         k.rt = (int)(item - (int64_t)k.h * k.tiles);
     }
     __device__ __forceinline__ void next_item(Cursor& k) const {
@@ -125,83 +143,101 @@ struct Work {
     }
 };
 
-// The line of all steps: its length, and the sequence that holds step u with
-// the steps before it.  Every thread of the CTA calls it; `sums` is kThreads + 1
-// words of shared memory.
+// The line of all steps, by one warp (every warp on its own, no barrier): lane
+// x holds `per` sequences from x * per on, and the steps before them.
 template <int NT, bool LIST>
-__device__ int64_t line_sums(const Work<NT, LIST>& w, int64_t* sums, uint32_t* status) {
-    const int tid = threadIdx.x, nb = w.p.c.batch, per = (nb + kThreads - 1) / kThreads;
-    int64_t s = 0;
-    for (int i = 0; i < per; ++i) {
-        const int b = tid * per + i;
-        if (b < nb) {
-            Cursor k;
-            w.load(k, b, status);
-            s += w.total(k);
+struct LineOf {
+    int64_t before, total;
+    int per;
+    Cursor mine;    // of this lane's sequence when per == 1
+
+    __device__ __forceinline__ LineOf(const Work<NT, LIST>& w, uint32_t* status) {
+        const int lane = threadIdx.x & 31, nb = w.p.c.batch;
+        per = (nb + 31) >> 5;
+        int64_t s = 0;
+        for (int i = 0; i < per; ++i) {
+            w.load(mine, lane * per + i, status);
+            s += w.total(mine);
         }
-    }
-    int64_t inc = s;
+        int64_t inc = s;
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const int64_t v = __shfl_up_sync(0xFFFFFFFFu, inc, o);
-        if ((tid & 31) >= o) inc += v;
+        for (int o = 1; o < 32; o <<= 1) {
+            const int64_t v = __shfl_up_sync(0xFFFFFFFFu, inc, o);
+            if (lane >= o) inc += v;
+        }
+        before = inc - s;
+        total = __shfl_sync(0xFFFFFFFFu, inc, 31);
     }
-    sums[tid + 1] = inc;
-    __syncthreads();
-    int64_t base = 0;
-    for (int i = 0; i < (tid >> 5); ++i) base += sums[(i + 1) * 32];
-    __syncthreads();
-    sums[tid + 1] = base + inc;
-    if (tid == 0) sums[0] = 0;
-    __syncthreads();
-    return sums[kThreads];
-}
+    // The step u (0 <= u < total) as a cursor.
+    __device__ __forceinline__ void find(const Work<NT, LIST>& w, int64_t u, Cursor& k) const {
+        const int at = 31 - __clz(__ballot_sync(0xFFFFFFFFu, before <= u));
+        u -= __shfl_sync(0xFFFFFFFFu, before, at);
+        if (per == 1) {
+            k.b = at;
+            k.steps = __shfl_sync(0xFFFFFFFFu, mine.steps, at);
+            k.tiles = __shfl_sync(0xFFFFFFFFu, mine.tiles, at);
+            k.L = __shfl_sync(0xFFFFFFFFu, mine.L, at);
+            k.n = __shfl_sync(0xFFFFFFFFu, mine.n, at);
+            k.lo = __shfl_sync(0xFFFFFFFFu, mine.lo, at);
+        } else {
+            for (int b = at * per;; ++b) {
+                w.load(k, b, nullptr);
+                const int64_t t = w.total(k);
+                if (u < t || b + 1 >= w.p.c.batch) break;
+                u -= t;
+            }
+        }
+        w.seek(k, u);
+    }
+};
 
-// The step u (0 <= u < total) as a cursor.
-template <int NT, bool LIST>
-__device__ void line_find(const Work<NT, LIST>& w, const int64_t* sums, int64_t u, Cursor& k) {
-    const int nb = w.p.c.batch, per = (nb + kThreads - 1) / kThreads;
-    int lo = 0, hi = kThreads;  // sums[lo] <= u < sums[hi]
-    while (hi - lo > 1) {
-        const int mid = (lo + hi) >> 1;
-        if (sums[mid] <= u) lo = mid;
-        else hi = mid;
+// The line in `share` pieces: the first `more` of them one step longer than `size`.
+struct Pieces {
+    int64_t size, more;
+    int share;
+    __device__ __forceinline__ Pieces(int64_t total, int ctas) {
+        share = total < ctas ? (total < 1 ? 1 : (int)total) : ctas;
+        size = quotient(total, share);
+        more = total - size * share;
     }
-    u -= sums[lo];
-    int b = lo * per;
-    for (;; ++b) {
-        w.load(k, b, nullptr);
-        const int64_t t = w.total(k);
-        if (u < t || b + 1 >= nb) break;
-        u -= t;
+    __device__ __forceinline__ int64_t start(int x) const { return size * x + (x < more ? x : more); }
+    __device__ __forceinline__ int holding(int64_t u) const {   // the piece with step u
+        const int64_t longer = more * (size + 1);
+        return (int)(u < longer ? quotient(u, size + 1) : more + quotient(u - longer, size));
     }
-    w.seek(k, u);
-}
+};
 
-// How many CTAs share `total` steps.
-__device__ __forceinline__ int64_t sharing(int64_t total, int ctas) {
-    return total < ctas ? (total < 1 ? 1 : total) : ctas;
-}
+// What a computing warp is told of a tile: the first position of both groups of
+// 16 (-1: nothing there) and their scales; and of an item.
+struct Tile {
+    int t0, t1;
+    float ks0, ks1, vs0, vs1;
+};
+struct Item {
+    Cursor k;
+    int todo, flags;        // steps of the piece; 1: from the item's first step, 2: to its last
+    int parts;              // pieces the item lies in, from this one on
+};
 
 template <int D, int NT>
 struct Smem {
     static constexpr int kRows = kTile * D;          // bytes of one tile's keys (or values)
-    // a warp computes on one stage while the others fill: two are enough with three CTAs an SM
-    static constexpr int kStages = (NT <= 2 ? 2 : 3) * (128 / D);
+    static constexpr int kStages = 3 * (128 / D);
+    static constexpr int kItems = 4;                 // items looked ahead
     static constexpr int ring = 0;                                            // [warp][stage][K, V]
     static constexpr int merge = ring + kWarps * kStages * 2 * kRows;         // [warp][16][32] floats
     static constexpr int stats = merge + kWarps * 16 * 32 * 4;                // [warp][8 * NT][3] floats
-    static constexpr int slots = stats + kWarps * 8 * NT * 3 * 4;             // [warp][stage] int4
-    static constexpr int bars = slots + kWarps * kStages * 16;                // [warp][stage]
-    static constexpr int sums = merge;                                        // kThreads + 1 words, before the first merge
-    static constexpr int bytes = bars + kWarps * kStages * 8 + 1024;          // base aligned to 1024
+    static constexpr int tiles = stats + kWarps * 8 * NT * 3 * 4;             // [warp][stage]
+    static constexpr int items = tiles + kWarps * kStages * 32;               // [kItems]
+    static constexpr int bars = items + kItems * 64;                          // full, empty [warp][stage]; items full, empty
+    static constexpr int bytes = bars + (2 * kWarps * kStages + 2 * kItems) * 8 + 1024;   // base aligned to 1024
 };
 
-// Partial of a cut item: [32 rows][D] outputs, per row (m, l, M), then what
+// Partial of a cut item: [16 rows][D] outputs, per row (m, l, M), then what
 // k_kv8_combine needs of the item: b, h, rt, rows, and how many pieces it has.
 template <int D>
 struct Part {
-    static constexpr int kStats = 32 * D, kDesc = kStats + 32 * 3, kFloats = kDesc + 32;
+    static constexpr int kStats = 16 * D, kDesc = kStats + 16 * 3, kFloats = kDesc + 16;
 };
 
 // Four adjacent outputs x * f, rounded once to the query's type.
@@ -229,149 +265,231 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
 
 // NT: tiles of eight query rows.
 template <int D, int NT, bool LIST>
-__global__ void __launch_bounds__(kThreads, NT <= 2 ? 3 : 2) k_kv8_attn(const __grid_constant__ Params p,
-                                                                        const __grid_constant__ CUtensorMap kmap,
-                                                                        const __grid_constant__ CUtensorMap vmap) {
+__global__ void __launch_bounds__(kThreads, kPerSm) k_kv8_attn(const __grid_constant__ Params p,
+                                                               const __grid_constant__ CUtensorMap kmap,
+                                                               const __grid_constant__ CUtensorMap vmap) {
     using S = Smem<D, NT>;
     constexpr int kChunks = D / 64;   // 16-byte chunks of a key row per lane
     constexpr int kCh = D / 8;        // channels of a value row per lane
     constexpr int kStages = S::kStages;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = smem_raw + ((1024u - (tc::smem_u32(smem_raw) & 1023u)) & 1023u);
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, r = lane >> 2, c = lane & 3;
-    uint8_t* ring = smem + S::ring + warp * kStages * 2 * S::kRows;
-    int4* slots = reinterpret_cast<int4*>(smem + S::slots) + warp * kStages;
-    uint64_t* bars = reinterpret_cast<uint64_t*>(smem + S::bars) + warp * kStages;
-    int64_t* sums = reinterpret_cast<int64_t*>(smem + S::sums);
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    uint64_t* bars = reinterpret_cast<uint64_t*>(smem + S::bars);          // full [warp][stage]
+    uint64_t* empty = bars + kWarps * kStages;                             // [warp][stage]
+    uint64_t* item_full = empty + kWarps * kStages;                        // [kItems]
+    uint64_t* item_empty = item_full + S::kItems;
+    Item* items = reinterpret_cast<Item*>(smem + S::items);
     const int bs = p.c.bs(), G = p.G, T = p.a.q.T, H = p.a.q.H;
-    const bool pairs = bs == kGroup;  // a tile is two blocks
-    if (lane == 0) {
-        for (int i = 0; i < kStages; ++i) tc::mbar_init(bars + i, 1);
+    if (tid == 0) {
+        for (int i = 0; i < kWarps * kStages; ++i) {
+            tc::mbar_init(bars + i, 1);
+            tc::mbar_init(empty + i, 1);
+        }
+        for (int i = 0; i < S::kItems; ++i) {
+            tc::mbar_init(item_full + i, 1);
+            tc::mbar_init(item_empty + i, kWarps);
+        }
         tc::fence_mbar_init();
     }
     pdl_begin();
+    __syncthreads();
     const Work<NT, LIST> work(p);
-    const int64_t total = line_sums(work, sums, blockIdx.x == 0 ? p.a.status : nullptr);
-    const int64_t share = sharing(total, p.ctas);
     int* desc = reinterpret_cast<int*>(p.a.part + ((int64_t)blockIdx.x * 2 + 1) * Part<D>::kFloats + Part<D>::kDesc);
-    if (tid == 0) desc[4] = 0;
-    if (blockIdx.x >= share) return;
-    const int64_t u0 = total * blockIdx.x / share, u1 = total * (blockIdx.x + 1) / share;
-    if (u0 >= u1) return;
 
-    Cursor cur, ahead;
-    line_find(work, sums, u0, cur);
-    ahead = cur;
-    __syncthreads();         // `sums` is the merge buffer's
+    if (warp == kWarps) {
+        // ------------------------------------------------------------ the warp that looks ahead
+        if (lane == 0) desc[4] = 0;
+        const LineOf<NT, LIST> line(work, blockIdx.x == 0 ? p.a.status : nullptr);
+        const Pieces pieces(line.total, p.ctas);
+        const bool any = line.total > 0 && blockIdx.x < pieces.share;
+        const int64_t u0 = any ? pieces.start(blockIdx.x) : 0, u1 = any ? pieces.start(blockIdx.x + 1) : 0;
+        int steps = (int)(u1 - u0);
+        Cursor cur;
+        if (any) line.find(work, u0, cur);
+        const bool pairs = bs == kGroup;      // a tile is two blocks
+        const int w = lane & (kWarps - 1);    // this lane's warp (lanes 0 .. 3 act)
+        bool alive = true;
+        uint32_t copies = 0;                  // slots with a copy in flight that nobody waits for (bit mask)
 
-    // ---- the copies: the ring runs ahead of the tiles by kStages - 1.  A
-    // tile's block is looked up two tiles before its copy is issued (the list
-    // entry) and one tile before (the page table), so neither load is waited for.
-    int64_t ahead_u = u0;
-    int look_b = 0, look_h = 0, look_row = 0, look_lb[2];
-    auto peek = [&]() {      // describe the tile at `ahead`, start its list loads, move on
-        look_lb[0] = look_lb[1] = -1;
-        look_b = ahead.b;
-        look_h = ahead.h;
-        if (ahead_u >= u1) return;
-        const int off = ahead.step * kStep + warp * kTile;
-        if (LIST) {
-            const int j = ahead.rt / p.gt, pos = ahead.L - ahead.n + j;
-            const int32_t* l = p.a.block_idx + (((int64_t)ahead.b * T + j) * p.c.heads + ahead.h) * p.a.n_sel;
-            look_row = off & (bs - 1);
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                const int e = (off >> p.c.bs_log2) + i;
-                if ((i && !pairs) || e >= p.a.n_sel) break;
-                const int v = __ldg(l + e), prev = e ? __ldg(l + e - 1) : -1;
-                if (v >= 0) {
-                    // strictly ascending, visible, nothing behind padding: anything else is skipped and flagged
-                    if (pos < 0 || v > (pos >> p.c.bs_log2) || (e && v <= prev) || (e && prev < 0)) {
-                        if (lane == 0) flag(p.a.status, kStatusBounds);
-                    } else {
-                        look_lb[i] = v;
-                    }
-                } else if (v < -1 && lane == 0) {
-                    flag(p.a.status, kStatusBounds);
+        // A step goes through four stages, each a load that the next one needs: list entries, pages,
+        // scales, and the copy; the steps behind it are one stage further back.
+        struct Look {
+            int b, h, row, lb[2], phys[2];
+            float ks[2], vs[2];
+        };
+        int64_t ahead_u = u0;
+        int item_no = 0;
+        Cursor at = cur;
+        int todo_left = steps, in_item = 0;   // steps of the piece not yet looked at; of the item at `at`
+        auto entries = [&](Look& k) {         // stage 1, and the items as they come up
+            k.lb[0] = k.lb[1] = -1;
+            k.b = at.b;
+            k.h = at.h;
+            k.row = 0;
+            if (todo_left == 0) return;
+            if (in_item == 0) {
+                const int left = at.steps - at.step, todo = todo_left < left ? todo_left : left, i = item_no % S::kItems;
+                if (item_no >= S::kItems && alive) {
+                    alive = tc::mbar_wait(item_empty + i, ((item_no / S::kItems) - 1) & 1, p.wait_limit);
+                    if (!alive && lane == 0) flag(p.a.status, kStatusTimeout);
+                    alive = __all_sync(0xFFFFFFFFu, alive);
                 }
+                if (lane == 0) {
+                    items[i].k = at;
+                    items[i].todo = todo;
+                    items[i].flags = (at.step == 0 ? 1 : 0) | (todo == left ? 2 : 0);
+                    items[i].parts = pieces.holding(ahead_u + left - 1) - (int)blockIdx.x + 1;
+                    tc::mbar_arrive(item_full + i);
+                }
+                __syncwarp();
+                ++item_no;
+                in_item = todo;
             }
-        } else {
-            const int t = ahead.lo + off;
-            look_row = t & (bs - 1);
-            if (t < ahead.L) look_lb[0] = t >> p.c.bs_log2;
-            if (pairs && t + kGroup < ahead.L) look_lb[1] = look_lb[0] + 1;
-        }
-        ++ahead_u;
-        if (++ahead.step >= ahead.steps) work.next_item(ahead);
-    };
-    int hand_h = 0, hand_row = 0, hand_lb[2], hand_phys[2];
-    auto lookup = [&]() {    // the pages of the tile peeked at
-        hand_h = look_h;
-        hand_row = look_row;
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            hand_lb[i] = look_lb[i];
-            hand_phys[i] = -1;
-            if (look_lb[i] >= 0) {
-                hand_phys[i] = kv8_block(p.c, look_b, look_lb[i]);
-                if (hand_phys[i] < 0 && lane == 0) flag(p.a.status, kStatusBounds);
-            }
-        }
-    };
-    bool alive = true;       // false once a wait ran out: no further copies, no further results
-    uint32_t late = 0;       // slots whose copies were given up on (bit mask)
-    auto issue = [&](int slot) {
-        if (lane == 0) {
-            // (unit, first position) of both groups of 16; unit = physical block * heads + head, -1: nothing there
-            int4 d = make_int4(-1, 0, -1, 0);
-            if (alive && (hand_phys[0] >= 0 || hand_phys[1] >= 0)) {
-                uint8_t* kd = ring + slot * 2 * S::kRows;
-                const int n = pairs ? (hand_phys[0] >= 0) + (hand_phys[1] >= 0) : 2;   // groups that arrive
-                tc::mbar_arrive_expect_tx(bars + slot, n * S::kRows);
+            const int off = at.step * kStep + w * kTile;
+            if (LIST) {
+                const int j = at.rt / p.gt, pos = at.L - at.n + j;
+                const int32_t* l = p.a.block_idx + (((int64_t)at.b * T + j) * p.c.heads + at.h) * p.a.n_sel;
+                k.row = off & (bs - 1);
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
-                    if (hand_phys[i] < 0) continue;
-                    const int unit = hand_phys[i] * p.c.heads + hand_h;
-                    const int row = (unit << p.c.bs_log2) + hand_row;
-                    tc::tma_load_2d(kd + i * kGroup * D, &kmap, 0, row, bars + slot);
-                    tc::tma_load_2d(kd + S::kRows + i * kGroup * D, &vmap, 0, row, bars + slot);
-                    if (i == 0) d.x = unit, d.y = (hand_lb[0] << p.c.bs_log2) + hand_row;
-                    else d.z = unit, d.w = hand_lb[1] << p.c.bs_log2;
+                    const int e = (off >> p.c.bs_log2) + i;
+                    if ((i && !pairs) || e >= p.a.n_sel) break;
+                    const int v = __ldg(l + e), prev = e ? __ldg(l + e - 1) : -1;
+                    if (v >= 0) {
+                        // strictly ascending, visible, nothing behind padding: anything else is skipped and flagged
+                        if (pos < 0 || v > (pos >> p.c.bs_log2) || (e && v <= prev) || (e && prev < 0)) {
+                            if (lane < kWarps) flag(p.a.status, kStatusBounds);
+                        } else {
+                            k.lb[i] = v;
+                        }
+                    } else if (v < -1 && lane < kWarps) {
+                        flag(p.a.status, kStatusBounds);
+                    }
                 }
-                if (!pairs) d.z = d.x, d.w = d.y + kGroup;
+            } else {
+                const int t = at.lo + off;
+                k.row = t & (bs - 1);
+                if (t < at.L) k.lb[0] = t >> p.c.bs_log2;
+                if (pairs && t + kGroup < at.L) k.lb[1] = k.lb[0] + 1;
             }
-            slots[slot] = d;
-        }
-    };
-
-    peek();
-    lookup();
-    peek();
+            ++ahead_u;
+            --todo_left;
+            --in_item;
+            if (++at.step >= at.steps) work.next_item(at);
+        };
+        auto pages = [&](Look& k) {           // stage 2
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                k.phys[i] = k.lb[i] >= 0 ? kv8_block(p.c, k.b, k.lb[i]) : -1;
+                if (k.lb[i] >= 0 && k.phys[i] < 0 && lane < kWarps) flag(p.a.status, kStatusBounds);
+            }
+        };
+        auto scales = [&](Look& k) {          // stage 3
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                k.ks[i] = k.vs[i] = 1.0f;
+                if (k.phys[i] >= 0) {
+                    const int64_t unit = (int64_t)k.phys[i] * p.c.heads + k.h;
+                    k.ks[i] = __ldg(p.c.k_scale + unit);
+                    k.vs[i] = __ldg(p.c.v_scale + unit);
+                }
+            }
+        };
+        Look k1, k2, k3;
+        entries(k1);
+        k2 = k1;
+        pages(k2);
+        entries(k1);
+        k3 = k2;
+        scales(k3);
+        k2 = k1;
+        pages(k2);
+        entries(k1);
+        int slot = 0, round = 0;
 #pragma unroll 1
-    for (int i = 0; i < kStages - 1; ++i) {
-        issue(i);
-        lookup();
-        peek();
+        for (int s = 0; s < steps; ++s) {
+            if (round > 0 && alive && lane < kWarps) {   // the warp has read the slot's last tile
+                alive = tc::mbar_wait(empty + w * kStages + slot, (round - 1) & 1, p.wait_limit);
+                if (!alive) flag(p.a.status, kStatusTimeout);
+            }
+            alive = __all_sync(0xFFFFFFFFu, alive);
+            if (!alive) break;
+            if (lane < kWarps) {
+                uint8_t* kd = smem + S::ring + (w * kStages + slot) * 2 * S::kRows;
+                uint64_t* bar = bars + w * kStages + slot;
+                const int n = pairs ? (k3.phys[0] >= 0) + (k3.phys[1] >= 0) : k3.phys[0] >= 0 ? 2 : 0;   // groups that arrive
+                tc::mbar_expect_tx(bar, n * S::kRows);
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    if (k3.phys[i] < 0) continue;
+                    const int row = ((k3.phys[i] * p.c.heads + k3.h) << p.c.bs_log2) + k3.row;
+                    tc::tma_load_2d(kd + i * kGroup * D, &kmap, 0, row, bar);
+                    tc::tma_load_2d(kd + S::kRows + i * kGroup * D, &vmap, 0, row, bar);
+                }
+                Tile d = {-1, -1, k3.ks[0], k3.ks[1], k3.vs[0], k3.vs[1]};
+                if (k3.phys[0] >= 0) d.t0 = (k3.lb[0] << p.c.bs_log2) + k3.row;
+                if (pairs) {
+                    if (k3.phys[1] >= 0) d.t1 = k3.lb[1] << p.c.bs_log2;
+                } else {
+                    if (n) d.t1 = d.t0 + kGroup;
+                    d.ks1 = d.ks0;
+                    d.vs1 = d.vs0;
+                }
+                reinterpret_cast<Tile*>(smem + S::tiles + (w * kStages + slot) * 32)[0] = d;
+                tc::mbar_arrive(bar);
+                copies |= 1u << slot;
+            }
+            if (++slot == kStages) slot = 0, ++round;
+            k3 = k2;
+            scales(k3);
+            k2 = k1;
+            pages(k2);
+            entries(k1);
+        }
+        // the end of the line: an item without steps
+        if (alive) {
+            const int i = item_no % S::kItems;
+            if (item_no >= S::kItems) alive = __all_sync(0xFFFFFFFFu, tc::mbar_wait(item_empty + i, ((item_no / S::kItems) - 1) & 1, p.wait_limit));
+            if (lane == 0 && alive) {
+                items[i].todo = 0;
+                tc::mbar_arrive(item_full + i);
+            }
+        }
+        // what was copied last still lands in this CTA's memory
+        if (lane < kWarps) {
+            for (int i = 0; i < kStages; ++i) {
+                const int last_round = i < slot ? round : round - 1;   // of the slot's last copy
+                if ((copies >> i) & 1u) tc::mbar_wait(bars + w * kStages + i, last_round & 1);
+            }
+        }
+        return;
     }
-    __syncwarp();
+
+    // ---------------------------------------------------------------- a computing warp
+    const int r = lane >> 2, c = lane & 3;
+    uint8_t* ring = smem + S::ring + warp * kStages * 2 * S::kRows;
+    bars += warp * kStages;
+    empty += warp * kStages;
+    // The computing warps meet; they all leave together once a wait of one of them ran out.
+    auto meet = [] { asm volatile("bar.sync 1, 128;" ::: "memory"); };
+    bool alive = true;       // false once a wait ran out: no further results
     int slot = 0;
     uint32_t phase = 0;      // parity of each slot's barrier (bit mask)
-    int4 here = slots[0];
-    float ks[2], vs[2];      // scales of the tile's groups
-    auto scales = [&]() {
-        ks[0] = here.x >= 0 ? __ldg(p.c.k_scale + here.x) : 0.0f;
-        vs[0] = here.x >= 0 ? __ldg(p.c.v_scale + here.x) : 1.0f;
-        ks[1] = here.z >= 0 ? __ldg(p.c.k_scale + here.z) : 0.0f;
-        vs[1] = here.z >= 0 ? __ldg(p.c.v_scale + here.z) : 1.0f;
-    };
-    scales();
-
-    int64_t u = u0;
-    while (u < u1) {
-        const bool from_start = cur.step == 0;
-        const int item_left = cur.steps - cur.step;
-        const int todo = u1 - u < item_left ? (int)(u1 - u) : item_left;
-        const bool to_end = todo == item_left;
+    for (int item_no = 0;; ++item_no) {
+        Item* item = items + item_no % S::kItems;
+        {
+            bool ok = tc::mbar_wait(item_full + item_no % S::kItems, (item_no / S::kItems) & 1, p.wait_limit) && alive;
+            if (!ok) flag(p.a.status, kStatusTimeout);
+            int go;
+            asm volatile("{\n\t.reg .pred a, b;\n\tsetp.ne.b32 a, %1, 0;\n\t"
+                         "barrier.cta.red.and.pred b, 1, 128, a;\n\tselp.b32 %0, 1, 0, b;\n\t}"
+                         : "=r"(go) : "r"((int)ok) : "memory");
+            if (!go) return;
+        }
+        const Cursor cur = item->k;
+        const int todo = item->todo;
+        if (todo == 0) return;
         const int rows = work.rows(cur);
 
         // ---- query row r of every tile of eight, in operand layout
@@ -459,31 +577,24 @@ __global__ void __launch_bounds__(kThreads, NT <= 2 ? 3 : 2) k_kv8_attn(const __
 
 #pragma unroll 1
         for (int i = 0; i < todo; ++i) {
-            // refill the slot that was read last, then look at the next tile's scales
-            issue(slot == 0 ? kStages - 1 : slot - 1);
-            lookup();
-            peek();
-            const int4 tile = here;
-            const float ks_now[2] = {ks[0], ks[1]}, vs_now[2] = {vs[0], vs[1]};
-            const int now = slot;
-            slot = slot + 1 == kStages ? 0 : slot + 1;
-            __syncwarp();
-            here = slots[slot];
-            scales();
-            if (tile.x < 0 && tile.z < 0) continue;
             if (alive) {
-                alive = tc::mbar_wait(bars + now, (phase >> now) & 1u, p.wait_limit);
+                alive = tc::mbar_wait(bars + slot, (phase >> slot) & 1u, p.wait_limit);
                 if (!alive && lane == 0) flag(p.a.status, kStatusTimeout);
             }
             alive = __all_sync(0xFFFFFFFFu, alive);
-            if (!alive) {
-                late |= 1u << now;
+            if (!alive) break;
+            phase ^= 1u << slot;
+            const Tile tile = *reinterpret_cast<const Tile*>(smem + S::tiles + (warp * kStages + slot) * 32);
+            uint8_t* kt = ring + slot * 2 * S::kRows;
+            uint8_t* vt = kt + S::kRows;
+            uint64_t* done = empty + slot;
+            slot = slot + 1 == kStages ? 0 : slot + 1;
+            if (tile.t0 < 0 && tile.t1 < 0) {
+                if (lane == 0) tc::mbar_arrive(done);
                 continue;
             }
-            phase ^= 1u << now;
-            uint8_t* kt = ring + now * 2 * S::kRows;
-            uint8_t* vt = kt + S::kRows;
-            const bool inside = tile.x >= 0 && tile.z >= 0 && tile.y >= see0 && tile.w + kGroup - 1 <= see1;
+            const float ks_now[2] = {tile.ks0, tile.ks1}, vs_now[2] = {tile.vs0, tile.vs1};
+            const bool inside = tile.t0 >= 0 && tile.t1 >= 0 && tile.t0 >= see0 && tile.t1 + kGroup - 1 <= see1;
             if (!inside) {
                 // what lies behind the sequence's end, or was not copied, may be any code: NaN times a
                 // weight of 0 is NaN, so those value rows are cleared
@@ -492,7 +603,7 @@ __global__ void __launch_bounds__(kThreads, NT <= 2 ? 3 : 2) k_kv8_attn(const __
                 for (int g = 0; g < 2; ++g)
                     for (int x = lane; x < kGroup * (D / 16); x += 32) {
                         const int row = x / (D / 16);
-                        if ((g ? tile.z : tile.x) < 0 || (g ? tile.w : tile.y) + row >= cur.L) {
+                        if ((g ? tile.t1 : tile.t0) < 0 || (g ? tile.t1 : tile.t0) + row >= cur.L) {
                             *reinterpret_cast<uint4*>(vt + g * kGroup * D + x * 16) = make_uint4(0, 0, 0, 0);
                             cleared = true;
                         }
@@ -552,12 +663,12 @@ __global__ void __launch_bounds__(kThreads, NT <= 2 ? 3 : 2) k_kv8_attn(const __
             if (!inside) {
 #pragma unroll
                 for (int g = 0; g < 2; ++g) {
-                    const bool there = (g ? tile.z : tile.x) >= 0;
+                    const bool there = (g ? tile.t1 : tile.t0) >= 0;
 #pragma unroll
                     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                         for (int e = 0; e < 4; ++e) {
-                            const int t = (g ? tile.w : tile.y) + r + (e >> 1) * 8, pr = pos[nt][e & 1];
+                            const int t = (g ? tile.t1 : tile.t0) + r + (e >> 1) * 8, pr = pos[nt][e & 1];
                             const bool in = there && t <= pr && (LIST || !p.a.window || t > pr - p.a.window);
                             s[g][nt][e] = in ? s[g][nt][e] : -INFINITY;
                         }
@@ -644,6 +755,7 @@ __global__ void __launch_bounds__(kThreads, NT <= 2 ? 3 : 2) k_kv8_attn(const __
                 }
             }
             __syncwarp();
+            if (lane == 0) tc::mbar_arrive(done);
         }
 
         // ---- the four warps' parts of this item become one
@@ -662,7 +774,7 @@ __global__ void __launch_bounds__(kThreads, NT <= 2 ? 3 : 2) k_kv8_attn(const __
                     s3[2] = M[nt][e];
                 }
             }
-        __syncthreads();
+        meet();
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -687,7 +799,7 @@ __global__ void __launch_bounds__(kThreads, NT <= 2 ? 3 : 2) k_kv8_attn(const __
                 }
             }
         // a pass: eight rows, eight of each lane's channels; warp w sums four of them for row 2c + (w & 1)
-        const bool whole = from_start && to_end;
+        const bool from_start = (item->flags & 1) != 0, to_end = (item->flags & 2) != 0, whole = from_start && to_end;
         float* part = p.a.part + ((int64_t)blockIdx.x * 2 + (from_start ? 1 : 0)) * Part<D>::kFloats;
         const int e = warp & 1, hh = warp >> 1;
 #pragma unroll
@@ -697,7 +809,7 @@ __global__ void __launch_bounds__(kThreads, NT <= 2 ? 3 : 2) k_kv8_attn(const __
             for (int ps = 0; ps < kCh / 8; ++ps) {
 #pragma unroll
                 for (int x = 0; x < 16; ++x) buf[(warp * 16 + x) * 32 + lane] = o[nt][ps * 4 + x / 4][x & 3];
-                __syncthreads();
+                meet();
                 const int row = nt * 8 + 2 * c + e;
                 if (row < rows && alive) {
                     float y[4];
@@ -728,25 +840,19 @@ __global__ void __launch_bounds__(kThreads, NT <= 2 ? 3 : 2) k_kv8_attn(const __
                         }
                     }
                 }
-                __syncthreads();
+                meet();
             }
         }
         if (from_start && !to_end && tid == 0) {  // the pieces up to the one with the item's last step
-            const int64_t last_u = u + item_left - 1;
-            const int64_t last = ((last_u + 1) * share + total - 1) / total - 1;
             desc[0] = cur.b;
             desc[1] = cur.h;
             desc[2] = cur.rt;
             desc[3] = rows;
-            desc[4] = (int)(last - blockIdx.x) + 1;
+            desc[4] = item->parts;
         }
-        u += todo;
-        cur.step += todo - 1;
-        if (++cur.step >= cur.steps) work.next_item(cur);
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive(item_empty + item_no % S::kItems);
     }
-    // copies that were given up on still land in this CTA's memory
-    for (int i = 0; i < kStages; ++i)
-        if ((late >> i) & 1u) tc::mbar_wait(bars + i, (phase >> i) & 1u);
 }
 
 // The items that the line's cuts went through: CTA x merges the item that
@@ -822,7 +928,6 @@ __global__ void __launch_bounds__(4 * D) k_kv8_combine(const __grid_constant__ P
 template <int D, int NT, bool LIST>
 cudaError_t launch(Params& p, cudaStream_t st) {
     using S = Smem<D, NT>;
-    constexpr int kPerSm = NT <= 2 ? 3 : 2;
     static_assert(S::bytes * kPerSm + kPerSm * 1024 <= 228 * 1024, "CTAs per SM");
     int dev = 0, sms = 0;
     cudaError_t e = cudaGetDevice(&dev);
@@ -847,7 +952,7 @@ cudaError_t launch_d(Params& p, cudaStream_t st) {
     if (p.a.block_idx) return p.G <= 8 ? launch<D, 1, true>(p, st) : launch<D, 2, true>(p, st);
     const int64_t rows = (int64_t)p.a.q.T * p.G;
     if (rows <= 8) return launch<D, 1, false>(p, st);
-    return rows <= 16 ? launch<D, 2, false>(p, st) : launch<D, 4, false>(p, st);
+    return launch<D, 2, false>(p, st);
 }
 
 }  // namespace
