@@ -551,8 +551,8 @@ def _kv8_ptr(cache, t, dtype, shape, what):
         return None
     if t.dtype is dtype and t.shape == shape and t.get_device() == cache.index and t.is_contiguous():
         return t.data_ptr()
-    if t.dtype != dtype or tuple(t.shape) != shape:
-        raise ValueError("%s is %s %s; got %s %s" % (what, dtype, shape, t.dtype, tuple(t.shape)))
+    if t.dtype != dtype or tuple(t.shape) != tuple(shape):
+        raise ValueError("%s is %s %s; got %s %s" % (what, dtype, tuple(shape), t.dtype, tuple(t.shape)))
     if t.device != cache.device:
         raise ValueError("%s is on %s, the cache on %s" % (what, t.device, cache.device))
     raise ValueError("%s must be contiguous" % what)
@@ -641,22 +641,26 @@ def kv8_read(cache, start_pos, k_out, v_out, n_rows=None, ws=None, stream=None):
               dt, _kv8_ws(cache, ws))
 
 
+_KV8_QUERY_DTYPES = {torch.bfloat16: BF16, torch.float16: F16}
+
+
 def _kv8_query(cache, q, n_q):
     """The query arguments of a call: address, type, strides, T, H, n_q."""
-    dt = _KV8_DTYPES.get(q.dtype)
-    if dt is None or dt == F32:
+    dt = _KV8_QUERY_DTYPES.get(q.dtype)
+    if dt is None:
         raise ValueError("q is bf16 or fp16; got %s" % q.dtype)
-    if q.dim() != 4:
+    shape = q.shape
+    if len(shape) != 4:
         raise ValueError("q is [batch, T, H, head_dim]")
-    _, T, H, _ = q.shape
-    qp, sb, st = _kv8_rows(cache, q, H, "q")
-    return qp, dt, sb, st, T, H, _kv8_ptr(cache, n_q, torch.int32, (cache.batch,), "n_q")
+    qp, sb, st = _kv8_rows(cache, q, shape[2], "q")
+    return (qp, dt, sb, st, shape[1], shape[2],
+            None if n_q is None else _kv8_ptr(cache, n_q, torch.int32, (cache.batch,), "n_q"))
 
 
 def _kv8_outputs(cache, q, out, lse, ws):
-    B, T, H, D = q.shape
-    return (_kv8_ptr(cache, out, q.dtype, (B, T, H, D), "out"), _kv8_ptr(cache, lse, torch.float32, (B, T, H), "lse"),
-            _kv8_ws(cache, ws), ws.numel() * ws.element_size())
+    shape = q.shape
+    return (_kv8_ptr(cache, out, q.dtype, shape, "out"),
+            None if lse is None else _kv8_ptr(cache, lse, torch.float32, shape[:3], "lse"), _kv8_ws(cache, ws), ws.nbytes)
 
 
 def kv8_attn(cache, q, out, ws, lse=None, window=0, n_q=None, sm_scale=0.0, stream=None):
@@ -675,7 +679,7 @@ def kv8_select_blocks(cache, q, block_idx, ws, n_first=0, n_recent=1, n_q=None, 
     args, n_sel = _kv8_query(cache, q, n_q), block_idx.shape[-1]
     _kv8_call(cache, stream, "kv8_select_blocks", lib().csa2_kv8_select_blocks, *args, n_sel, n_first, n_recent,
               _kv8_ptr(cache, block_idx, torch.int32, (cache.batch, args[4], cache.n_kv_heads, n_sel), "block_idx"),
-              _kv8_ws(cache, ws), ws.numel() * ws.element_size())
+              _kv8_ws(cache, ws), ws.nbytes)
 
 
 def kv8_block_attn(cache, q, block_idx, out, ws, lse=None, n_q=None, sm_scale=0.0, stream=None):
