@@ -8,15 +8,19 @@
 //   - four softmax warpgroups, two per row tile, a thread half a row (two
 //     halves a row keep a thread's 64 values in registers and halve the time
 //     from S to the weights, which is what the products wait for): read S from
-//     TMEM, agree on the running maximum, write the weights as fp16 over S (the
-//     second product takes them from TMEM), and rescale O on the rare step that
-//     moves the maximum by more than 2^4;
+//     TMEM, work out the weights with the maximum so far, and write them as
+//     fp16 over S (the second product takes them from TMEM) unless a weight
+//     came out above 2^7 of the maximum: then, rarely but for an item's first
+//     step, the halves agree on the new maximum, O is rescaled and the weights
+//     are worked out again;
 //   - a converter warpgroup: the codes of the next 128 positions from where TMA
 //     put them to fp16 operand tiles (E4M3 values are exact in fp16), two
 //     stages deep;
 //   - one warp that issues every tcgen05.mma.  It alternates the row tiles
 //     (O0 += P0 V, S0 = Q0 K, O1 += P1 V, S1 = Q1 K), so one tile's products
-//     run while the other's softmax does;
+//     run while the other's softmax does.  An item of at most 128 rows has one
+//     row tile: its even and odd steps then take the two places, each with a
+//     maximum, sum and output of its own, added up at the end;
 //   - one warp that looks up pages and issues the TMA loads.
 // Key scales multiply S per block; value scales enter the weights' exponent,
 // weight = 2^(z + log2(vs) - M), so the fp16 weights stay in range whatever the
@@ -42,7 +46,7 @@ constexpr int kMaxCtas = 148;
 constexpr int kMmaWarp = 20, kLoadWarp = 21;
 constexpr float kNone = -3.0e38f;
 constexpr float kHeadroom = 8.0f;   // weights are 2^(z - M + 8): full fp16 precision down to 2^-22
-constexpr float kLazy = 4.0f;       // and at most 2^12 before the maximum is moved
+constexpr float kLazy = 7.0f;       // and at most 2^15 (fp16: 65504) before the maximum is moved
 
 struct Params {
     DevKv8 c;
@@ -183,7 +187,7 @@ struct Smem {
     static constexpr int lims = sc + 8 * 8 * 8;               // [8] positions of a tile before the sequence's end
     static constexpr int xch = lims + 8 * 4;                  // [tile][half][128] floats: halves of a row agree
     static constexpr int bars = xch + 4 * 128 * 4;
-    static constexpr int misc = bars + 24 * 8;                // TMEM base, dead, failed[2]
+    static constexpr int misc = bars + 24 * 8;                // TMEM base, dead
     static constexpr int bytes = misc + 16;
 };
 
@@ -232,7 +236,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv8_prefill(const __grid_consta
         tc::mbar_init(bars + kO, 1);
         tc::mbar_init(bars + kDrain, 1);
         tc::fence_mbar_init();
-        misc[1] = misc[2] = misc[3] = 0;
+        misc[1] = 0;
     }
     pdl_begin();
     if (warp == kMmaWarp) tc::tmem_alloc(const_cast<uint32_t*>(misc), 512);
@@ -259,14 +263,19 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv8_prefill(const __grid_consta
         const uint32_t lanes = tmem + ((uint32_t)((warp & 3) * 32) << 16);
         const uint32_t col_s = lanes + t * 128, col_o = lanes + kColO + t * D + half * (D / 2);
         volatile float* xch = reinterpret_cast<volatile float*>(smem + S::xch) + t * 256;
-        // both halves of the tile's rows are here; false for all of them once one failed.  (A barrier for
-        // each two warps that share 32 rows, 64 threads, was slower, 343 against 314 us for 2,048 tokens over
-        // 8,192 positions: warps of a tile that drift apart delay the tile's products.)
-        auto agree = [&](bool ok) {
-            if (!ok) misc[2 + t] = 1;
-            asm volatile("bar.sync %0, 256;" ::"r"(1 + t) : "memory");
-            return misc[2 + t] == 0;
+        // Meetings of the threads of a tile (both halves of its rows) and of both tiles.  Whether all are
+        // well is part of the barrier itself, so that everyone goes the same way.  (A barrier for each two
+        // warps that share 32 rows, 64 threads, was slower, 343 against 314 us for 2,048 tokens over 8,192
+        // positions: warps of a tile that drift apart delay the tile's products.)
+        auto meet = [](int id, int threads, bool v) {
+            int r;
+            asm volatile("{\n\t.reg .pred a, b;\n\tsetp.ne.b32 a, %1, 0;\n\t"
+                         "barrier.cta.red.and.pred b, %2, %3, a;\n\tselp.b32 %0, 1, 0, b;\n\t}"
+                         : "=r"(r) : "r"((int)v), "r"(id), "r"(threads) : "memory");
+            return r != 0;
         };
+        auto agree = [&](bool v) { return meet(1 + t, 256, v); };
+        auto both_tiles = [&](bool v) { return meet(3, 512, v); };
         uint32_t tile = 0, s_phase = 0, o_phase = 0;   // tiles done by the CTA; parities
         bool ok = true;
         // Between items only this much of the cursor is kept (registers): the rest is worked out again.
@@ -279,18 +288,24 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv8_prefill(const __grid_consta
             k.step = step;
             return k;
         };
-        const int row = t * kTileRows + rt;
         while (todo_all > 0) {
             int todo, pos, first;
-            bool used;
+            bool dual;      // one row tile, even and odd steps apart
+            float e0;       // the value scale that sums are kept in: log2 of the item's first block's
             float zs = p.a.sm_scale * 1.4426950408889634f;
             {   // half a query row as fp16, K-major; bf16 scaled by the power of two that takes the row's
                 // greatest finite magnitude to [2^14, 2^15)
                 constexpr int kVec = D / 16;
                 const Cursor cur = item();
                 todo = todo_all < cur.steps - cur.step ? todo_all : cur.steps - cur.step;
-                used = t * kTileRows < cur.rows;
+                dual = cur.rows <= kTileRows;
+                const int row = dual ? rt : t * kTileRows + rt;
                 const bool mine = row < cur.rows;
+                const int at0 = cur.lo + cur.step * kPos;
+                const int block0 = at0 < cur.L ? kv8_block(p.c, cur.b, at0 >> p.c.bs_log2) : -1;
+                const float vs0 = block0 >= 0 ? __ldg(p.c.v_scale + (int64_t)block0 * p.c.heads + cur.h) : 1.0f;
+                const int e = (int)(__float_as_uint(vs0) >> 23) - 127;
+                e0 = e == -120 ? 0.0f : (float)(e < -100 ? -100 : (e > 100 ? 100 : e));
                 const int j = (cur.row0 + row) / G, g = cur.row0 + row - j * G;
                 pos = mine ? cur.L - cur.n + j : -1;
                 first = p.a.window ? pos - p.a.window + 1 : 0;
@@ -347,52 +362,68 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv8_prefill(const __grid_consta
                 tc::fence_proxy_async_smem();
                 tc::mbar_arrive(bars + kQ);
             }
-            float M = kNone, l = 0.0f, e0 = 0.0f;
+            float M = kNone, l = 0.0f;
+            bool started = false;      // O holds something
             for (int i = 0; i < todo; ++i, ++tile) {
-                if (!used) continue;
+                if (dual && (i & 1) != t) continue;
                 const int t0 = i * kPos;
                 ok = wait_warp(kS + t, s_phase) && ok;
                 s_phase ^= 1;
                 tc::fence_after_sync();
                 const float2* f2 = sc + (tile & 7) * 8 + half * 4;
-                uint32_t r[64];
-                tc::tmem_ld32_nowait(col_s + half * 64, r);
-                tc::tmem_ld32_nowait(col_s + half * 64 + 32, r + 32);
-                if (i == 0) {
-                    e0 = sc[(tile & 7) * 8].y;
-                    e0 = e0 < -100.0f ? -100.0f : (e0 > 100.0f ? 100.0f : e0);
-                }
                 // (factor of the logits, log2 of the value scale) of 16 positions
                 auto block = [&](int q) {
                     const float2 f = f2[q];
                     return make_float2(zs * f.x, f.y == -120.0f ? e0 : f.y);
                 };
-                tc::tmem_ld_wait();
-                if (!__all_sync(0xFFFFFFFFu, t0 + 63 <= pos && t0 >= first)) {
+                const bool edge = !__all_sync(0xFFFFFFFFu, t0 + 63 <= pos && t0 >= first);
+                uint32_t w[32];        // weights, two a word
+                float l1;
+#pragma unroll 1
+                for (;;) {
+                    uint32_t r[64];
+                    tc::tmem_ld32_nowait(col_s + half * 64, r);
+                    tc::tmem_ld32_nowait(col_s + half * 64 + 32, r + 32);
+                    tc::tmem_ld_wait();
+                    if (edge) {
 #pragma unroll
-                    for (int x = 0; x < 64; ++x)
-                        if (t0 + x > pos || t0 + x < first) r[x] = 0xFF800000u;
-                }
-                // ---- the greatest logit + log2(value scale) of the row
-                float top = -INFINITY;
+                        for (int x = 0; x < 64; ++x)
+                            if (t0 + x > pos || t0 + x < first) r[x] = 0xFF800000u;
+                    }
+                    float top = -INFINITY;     // the greatest logit + log2(value scale) of the half row
+                    l1 = 0.0f;
 #pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    float m = fmaxf(__uint_as_float(r[q * 16]), __uint_as_float(r[q * 16 + 1]));
+                    for (int q = 0; q < 4; ++q) {
+                        const uint32_t* v = r + q * 16;
+                        const float2 f = block(q);
+                        const float d = f.y - M + kHeadroom;
+                        const uint64_t ff = pack2(f.x, f.x), dd = pack2(d, d);
+                        uint64_t sum = 0;
+                        float m = __uint_as_float(v[0]);
 #pragma unroll
-                    for (int x = 2; x < 16; x += 2)
-                        m = max3(m, __uint_as_float(r[q * 16 + x]), __uint_as_float(r[q * 16 + x + 1]));
-                    const float2 f = block(q);
-                    top = fmaxf(top, m * f.x + f.y);
-                }
-                xch[half * 128 + rt] = top;
-                ok = agree(ok);      // and all of S is in registers: the weights may go over it
-                if (!ok) break;
-                top = fmaxf(top, xch[(half ^ 1) * 128 + rt]);
-                if (__any_sync(0xFFFFFFFFu, top > M + kLazy)) {
-                    const float M1 = fmaxf(M, top), f = ex2(M - M1);
+                        for (int x = 0; x < 16; x += 2) {
+                            m = x ? max3(m, __uint_as_float(v[x]), __uint_as_float(v[x + 1])) : fmaxf(m, __uint_as_float(v[1]));
+                            const float2 z = unpack2(fma2(pack2(__uint_as_float(v[x]), __uint_as_float(v[x + 1])), ff, dd));
+                            const float2 e = make_float2(ex2(z.x), ex2(z.y));
+                            sum = add2(sum, pack2(e.x, e.y));
+                            const __half2 h = __floats2half2_rn(e.x, e.y);
+                            memcpy(&w[q * 8 + x / 2], &h, 4);
+                        }
+                        top = fmaxf(top, m * f.x + f.y);
+                        // back from 2^(z + log2 vs - M + 8) to 2^(z + e0 - M + 8), exactly
+                        const float de = e0 - f.y;
+                        const float2 s2 = unpack2(sum);
+                        l1 += (s2.x + s2.y) * exp2_int(de < -126.0f ? -126 : (de > 126.0f ? 126 : (int)de));
+                    }
+                    // all of S is in registers from here: the weights may go over it
+                    if (agree(ok && !(top > M + kLazy))) break;
+                    xch[half * 128 + rt] = top;
+                    ok = agree(ok);
+                    if (!ok) break;
+                    const float M1 = fmaxf(M, fmaxf(top, xch[(half ^ 1) * 128 + rt])), f = ex2(M - M1);
                     l *= f;
                     M = M1;
-                    if (i > 0) {
+                    if (started) {
 #pragma unroll 1
                         for (int q = 0; q < D / 2; q += 16) {
                             uint32_t o[16];
@@ -403,30 +434,14 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv8_prefill(const __grid_consta
                             tc::tmem_st16_nowait(col_o + q, o);
                         }
                     }
+                    ok = agree(ok);            // the other half has read this one's maximum
+                    if (!ok) break;
                 }
-                // ---- weights over S, two to a column
-#pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    const uint32_t* v = r + q * 16;
-                    const float2 f = block(q);
-                    const float d = f.y - M + kHeadroom;
-                    const uint64_t ff = pack2(f.x, f.x), dd = pack2(d, d);
-                    uint64_t sum = 0;
-                    uint32_t w[8];
-#pragma unroll
-                    for (int x = 0; x < 16; x += 2) {
-                        const float2 z = unpack2(fma2(pack2(__uint_as_float(v[x]), __uint_as_float(v[x + 1])), ff, dd));
-                        const float2 e = make_float2(ex2(z.x), ex2(z.y));
-                        sum = add2(sum, pack2(e.x, e.y));
-                        const __half2 h = __floats2half2_rn(e.x, e.y);
-                        memcpy(&w[x / 2], &h, 4);
-                    }
-                    // back from 2^(z + log2 vs - M + 8) to 2^(z + e0 - M + 8), exactly
-                    const float de = e0 - f.y;
-                    const float2 s2 = unpack2(sum);
-                    l += (s2.x + s2.y) * exp2_int(de < -126.0f ? -126 : (de > 126.0f ? 126 : (int)de));
-                    tc::tmem_st8_nowait(col_s + half * 32 + q * 8, w);
-                }
+                if (!ok) break;
+                l += l1;
+                started = true;
+                tc::tmem_st16_nowait(col_s + half * 32, w);
+                tc::tmem_st16_nowait(col_s + half * 32 + 16, w + 16);
                 tc::tmem_st_wait();
                 tc::fence_before_sync();
                 tc::mbar_arrive(bars + kP + t);
@@ -437,17 +452,44 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv8_prefill(const __grid_consta
             tc::fence_after_sync();
             xch[half * 128 + rt] = l;
             ok = agree(ok);
-            if (!ok) break;
             l = half ? xch[rt] + l : l + xch[128 + rt];
             Cursor cur = item();
+            const int row = dual ? rt : t * kTileRows + rt;
             const bool mine = row < cur.rows;
             const int j = (cur.row0 + row) / G, g = cur.row0 + row - j * G, left = cur.steps - cur.step;
             const bool from_start = cur.step == 0, to_end = todo == left;
             const bool whole = from_start && to_end;
             float* part = p.a.part + ((int64_t)blockIdx.x * 2 + (from_start ? 1 : 0)) * Part<D>::kFloats;
             const int64_t at = ((int64_t)cur.b * T + j) * H + cur.h * G + g;
+            float f0 = 1.0f, f1 = 0.0f;            // factors of this tile's output and, dual, of the odd steps'
+            if (dual) {
+                float* odd = reinterpret_cast<float*>(smem + S::q);     // the odd steps' output [D][128], over the queries
+                volatile float* stats = reinterpret_cast<volatile float*>(smem + S::xch) + 256;   // their M and l
+                ok = agree(ok);
+                if (t == 1) {
+#pragma unroll 1
+                    for (int q = 0; q < D / 2; q += 16) {
+                        uint32_t o[16];
+                        tc::tmem_ld16_nowait(col_o + q, o);
+                        tc::tmem_ld_wait();
+#pragma unroll
+                        for (int x = 0; x < 16; ++x)
+                            odd[(half * (D / 2) + q + x) * 128 + rt] = started ? __uint_as_float(o[x]) : 0.0f;
+                    }
+                    if (half == 0) stats[rt] = M, stats[128 + rt] = l;
+                }
+                ok = both_tiles(ok);
+                if (t == 0) {
+                    const float M1 = stats[rt], l2 = stats[128 + rt], top = fmaxf(M, M1);
+                    f0 = ex2(M - top);
+                    f1 = ex2(M1 - top);
+                    l = l * f0 + l2 * f1;
+                    M = top;
+                }
+            }
             const float f = l == 0.0f ? 0.0f : exp2_int((int)e0) / l;
-            if (used) {
+            if (ok && (!dual || t == 0)) {
+                const float* odd = reinterpret_cast<const float*>(smem + S::q);
 #pragma unroll 1
                 for (int q = 0; q < D / 2; q += 32) {
                     uint32_t r[32];
@@ -455,6 +497,11 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv8_prefill(const __grid_consta
                     tc::tmem_ld_wait();
                     if (!mine) continue;
                     const int ch = half * (D / 2) + q;
+                    if (dual) {
+#pragma unroll
+                        for (int x = 0; x < 32; ++x)
+                            r[x] = __float_as_uint(__uint_as_float(r[x]) * f0 + odd[(ch + x) * 128 + rt] * f1);
+                    }
                     if (whole) {
                         uint4* dst = reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.a.out) + at * D + ch);
 #pragma unroll
@@ -494,7 +541,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv8_prefill(const __grid_consta
                     }
                 }
             }
-            if (from_start && !to_end && tid == 0) {
+            if (ok && from_start && !to_end && tid == 0) {
                 const int64_t last_u = u1 - todo_all + left - 1;
                 const int64_t last = ((last_u + 1) * share + total - 1) / total - 1;
                 desc[0] = cur.b;
@@ -504,6 +551,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv8_prefill(const __grid_consta
                 desc[4] = (int)(last - blockIdx.x) + 1;
             }
             tc::fence_before_sync();
+            ok = both_tiles(ok);       // (and the odd steps' outputs have been read: queries may go over them)
+            if (!ok) break;
             todo_all -= todo;
             if (todo_all > 0) {      // an item that goes on behind this piece is the last of it
                 line.next_item(cur);
@@ -619,11 +668,11 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv8_prefill(const __grid_consta
             const uint32_t tmem0 = __shfl_sync(0xFFFFFFFFu, tmem, 0);
             uint32_t tile = 0, q_phase = 0, p_phase = 0;
             bool ok = true;
-            auto scores = [&](int t, uint32_t st) {      // S_t = Q_t K^T
+            auto scores = [&](int t, int q, uint32_t st) {      // S_t = Q_q K^T
 #pragma unroll
                 for (int x = 0; x < D / 16; ++x) {
                     const uint32_t off = (x >> 2) * S::kPanel + (x & 3) * 32;
-                    tc::mma_f16(tmem0 + t * 128, tc::desc_at(dq, t * S::kTile + off), tc::desc_at(dk, st * S::kTile + off), idesc_s, x > 0);
+                    tc::mma_f16(tmem0 + t * 128, tc::desc_at(dq, q * S::kTile + off), tc::desc_at(dk, st * S::kTile + off), idesc_s, x > 0);
                 }
             };
             auto outputs = [&](int t, uint32_t st, bool more) {   // O_t += P_t V
@@ -650,11 +699,41 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv8_prefill(const __grid_consta
                 tiles = __shfl_sync(0xFFFFFFFFu, tiles, 0);
                 ok = wait_warp(kQ, q_phase);
                 q_phase ^= 1;
+                if (tiles == 1) {
+                    // steps alternate between the two places; a step's outputs come two steps later
+                    for (int i = 0; i < todo + 2 && ok; ++i, ++tile) {
+                        const int t = i & 1;
+                        const uint32_t st = tile & 1;            // stage of step i, and of step i - 2
+                        if (i >= 2) {
+                            ok = wait_warp(kVFull + st, ((tile - 2) >> 1) & 1u) && wait_warp(kP + t, (p_phase >> t) & 1u);
+                            if (!ok) break;
+                            p_phase ^= 1u << t;
+                            tc::fence_after_sync();
+                            if (tc::elect_one()) {
+                                outputs(t, st, i >= 4);
+                                tc::mma_commit(bars + kVEmpty + st);
+                            }
+                            __syncwarp();
+                        }
+                        if (i < todo) {
+                            ok = wait_warp(kKFull + st, (tile >> 1) & 1u);
+                            if (!ok) break;
+                            tc::fence_after_sync();
+                            if (tc::elect_one()) {
+                                scores(t, 0, st);
+                                tc::mma_commit(bars + kS + t);
+                                tc::mma_commit(bars + kKEmpty + st);
+                            }
+                            __syncwarp();
+                        }
+                    }
+                    tile -= 2;                                   // there is nothing behind the last step
+                } else
                 for (int i = 0; i <= todo && ok; ++i) {
                     const uint32_t st = tile & 1, prev = st ^ 1;     // stage of tile i, and of tile i - 1
                     if (i < todo) ok = wait_warp(kKFull + st, (tile >> 1) & 1u);
                     if (i > 0) ok = ok && wait_warp(kVFull + prev, ((tile - 1) >> 1) & 1u);
-                    for (int t = 0; t < tiles && ok; ++t) {
+                    for (int t = 0; t < 2 && ok; ++t) {
                         if (i > 0) {
                             ok = wait_warp(kP + t, (p_phase >> t) & 1u);
                             if (!ok) break;
@@ -662,7 +741,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv8_prefill(const __grid_consta
                             tc::fence_after_sync();
                             if (tc::elect_one()) {
                                 outputs(t, prev, i > 1);
-                                if (t == tiles - 1) tc::mma_commit(bars + kVEmpty + prev);
+                                if (t == 1) tc::mma_commit(bars + kVEmpty + prev);
                             }
                             __syncwarp();
                         } else {
@@ -670,9 +749,9 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv8_prefill(const __grid_consta
                         }
                         if (i < todo) {
                             if (tc::elect_one()) {
-                                scores(t, st);
+                                scores(t, t, st);
                                 tc::mma_commit(bars + kS + t);
-                                if (t == tiles - 1) tc::mma_commit(bars + kKEmpty + st);
+                                if (t == 1) tc::mma_commit(bars + kKEmpty + st);
                             }
                             __syncwarp();
                         }
