@@ -173,6 +173,13 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
     return r;
 }
 
+// log2 of the value scale that an item's sums are kept in, from its first
+// block's scale.
+__device__ __forceinline__ int sum_scale(float vs) {
+    const int e = (int)(__float_as_uint(vs) >> 23) - 127;
+    return e == -120 ? 0 : (e < -100 ? -100 : (e > 100 ? 100 : e));
+}
+
 template <int D>
 struct Smem {
     static constexpr int kPanels = D / 64;                    // 64 channels (128 bytes of fp16) a panel
@@ -183,11 +190,12 @@ struct Smem {
     static constexpr int v = k + 2 * kTile;                   // [stage][panel]
     static constexpr int codes = v + 2 * kTile;               // K, V as stored
     static constexpr int sums = codes;                        // kThreads + 1 words, before the first load
-    static constexpr int sc = codes + 2 * kPos * D;           // [8][8] (key scale, log2 value scale)
-    static constexpr int lims = sc + 8 * 8 * 8;               // [8] positions of a tile before the sequence's end
+    static constexpr int sc = codes + 2 * kPos * D;           // [8][8] key scale, log2 of the value scale
+    static constexpr int sg = sc + 8 * 8 * 8;                 // [8][8] 2^(e0 - that)
+    static constexpr int lims = sg + 8 * 8 * 4;               // [8] positions of a tile before the sequence's end
     static constexpr int xch = lims + 8 * 4;                  // [tile][half][128] floats: halves of a row agree
     static constexpr int bars = xch + 4 * 128 * 4;
-    static constexpr int misc = bars + 24 * 8;                // TMEM base, dead
+    static constexpr int misc = bars + 20 * 8;                // TMEM base, dead
     static constexpr int bytes = misc + 16;
 };
 
@@ -206,20 +214,22 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv8_prefill(const __grid_consta
     volatile uint32_t* misc = reinterpret_cast<volatile uint32_t*>(smem + S::misc);
     int64_t* sums = reinterpret_cast<int64_t*>(smem + S::sums);
     float2* sc = reinterpret_cast<float2*>(smem + S::sc);
+    float* sg = reinterpret_cast<float*>(smem + S::sg);
     volatile int* lims = reinterpret_cast<volatile int*>(smem + S::lims);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
-    // A bounded wait; once one ran out, every later wait of the CTA gives up too.
-    auto wait = [&](int bar, uint32_t parity) {
-        for (uint32_t i = 0; i < p.wait_limit; ++i) {
-            if (tc::mbar_try_wait(bars + bar, parity)) return true;
-            if (misc[1]) return false;
+    // A bounded wait of a warp; once one ran out, every later wait of the CTA gives up too.
+    auto wait_warp = [&](int bar, uint32_t parity) {
+        uint32_t n = 0;
+        bool ok;
+        do ok = p.wait_limit && __all_sync(0xFFFFFFFFu, tc::mbar_try_wait(bars + bar, parity));
+        while (!ok && ++n < p.wait_limit && !misc[1]);
+        if (!ok) {
+            if (!misc[1]) flag(p.a.status, kStatusTimeout);
+            misc[1] = 1;
         }
-        misc[1] = 1;
-        flag(p.a.status, kStatusTimeout);
-        return false;
+        return ok;
     };
-    auto wait_warp = [&](int bar, uint32_t parity) { return (bool)__all_sync(0xFFFFFFFFu, wait(bar, parity)); };
 
     if (tid == 0) {
         tc::mbar_init(bars + kQ, kSoftmax);
@@ -304,8 +314,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv8_prefill(const __grid_consta
                 const int at0 = cur.lo + cur.step * kPos;
                 const int block0 = at0 < cur.L ? kv8_block(p.c, cur.b, at0 >> p.c.bs_log2) : -1;
                 const float vs0 = block0 >= 0 ? __ldg(p.c.v_scale + (int64_t)block0 * p.c.heads + cur.h) : 1.0f;
-                const int e = (int)(__float_as_uint(vs0) >> 23) - 127;
-                e0 = e == -120 ? 0.0f : (float)(e < -100 ? -100 : (e > 100 ? 100 : e));
+                e0 = (float)sum_scale(vs0);
                 const int j = (cur.row0 + row) / G, g = cur.row0 + row - j * G;
                 pos = mine ? cur.L - cur.n + j : -1;
                 first = p.a.window ? pos - p.a.window + 1 : 0;
@@ -371,11 +380,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv8_prefill(const __grid_consta
                 s_phase ^= 1;
                 tc::fence_after_sync();
                 const float2* f2 = sc + (tile & 7) * 8 + half * 4;
-                // (factor of the logits, log2 of the value scale) of 16 positions
-                auto block = [&](int q) {
-                    const float2 f = f2[q];
-                    return make_float2(zs * f.x, f.y == -120.0f ? e0 : f.y);
-                };
+                const float* g1 = sg + (tile & 7) * 8 + half * 4;
                 const bool edge = !__all_sync(0xFFFFFFFFu, t0 + 63 <= pos && t0 >= first);
                 uint32_t w[32];        // weights, two a word
                 float l1;
@@ -395,9 +400,9 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv8_prefill(const __grid_consta
 #pragma unroll
                     for (int q = 0; q < 4; ++q) {
                         const uint32_t* v = r + q * 16;
-                        const float2 f = block(q);
-                        const float d = f.y - M + kHeadroom;
-                        const uint64_t ff = pack2(f.x, f.x), dd = pack2(d, d);
+                        const float2 f = f2[q];
+                        const float a = zs * f.x, d = f.y - M + kHeadroom;
+                        const uint64_t ff = pack2(a, a), dd = pack2(d, d);
                         uint64_t sum = 0;
                         float m = __uint_as_float(v[0]);
 #pragma unroll
@@ -409,11 +414,10 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv8_prefill(const __grid_consta
                             const __half2 h = __floats2half2_rn(e.x, e.y);
                             memcpy(&w[q * 8 + x / 2], &h, 4);
                         }
-                        top = fmaxf(top, m * f.x + f.y);
+                        top = fmaxf(top, m * a + f.y);
                         // back from 2^(z + log2 vs - M + 8) to 2^(z + e0 - M + 8), exactly
-                        const float de = e0 - f.y;
                         const float2 s2 = unpack2(sum);
-                        l1 += (s2.x + s2.y) * exp2_int(de < -126.0f ? -126 : (de > 126.0f ? 126 : (int)de));
+                        l1 += (s2.x + s2.y) * g1[q];
                     }
                     // all of S is in registers from here: the weights may go over it
                     if (agree(ok && !(top > M + kLazy))) break;
@@ -567,13 +571,13 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv8_prefill(const __grid_consta
         const int ct = tid - kSoftmax, l8 = ct & 7;
         // Piece (16 codes, two 16-byte chunks of fp16) `x` of this thread: eight lanes load 128 dense bytes'
         // worth of distinct banks and store to eight distinct ones.
-        auto convert = [&](const uint8_t* src, uint8_t* dst, int lim) {
+        auto convert = [&](const uint8_t* src, uint8_t* dst, bool clear, int lim) {
 #pragma unroll 4
             for (int x = 0; x < D / 16; ++x) {
                 const int row = D == 128 ? 2 * ((ct >> 3) + 16 * (x >> 1)) + ((l8 >> 2) ^ (x & 1)) : (ct >> 2) + 32 * x;
                 const int piece = D == 128 ? l8 : ct & 3;
                 uint4 w = *reinterpret_cast<const uint4*>(src + row * D + piece * 16);
-                if (row >= lim) w = make_uint4(0, 0, 0, 0);   // behind the sequence's end: zeros, whatever is there
+                if (clear && row >= lim) w = make_uint4(0, 0, 0, 0);
                 uint8_t* panel = dst + (piece >> 2) * S::kPanel;
                 const uint32_t c = (piece & 3) * 2;
                 *reinterpret_cast<uint4*>(panel + tc::sw128_offset(row, c)) =
@@ -589,14 +593,16 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv8_prefill(const __grid_consta
             if (tile >= 2) ok = ok && wait_warp(kKEmpty + st, ((tile >> 1) - 1) & 1);
             if (!ok) break;
             const int lim = lims[tile & 7];
-            convert(smem + S::codes, smem + S::k + st * S::kTile, lim);
+            convert(smem + S::codes, smem + S::k + st * S::kTile, false, 0);
             tc::fence_proxy_async_smem();
             tc::mbar_arrive(bars + kLEmpty);
             tc::mbar_arrive(bars + kKFull + st);
             ok = wait_warp(kLFull + 1, st);
             if (tile >= 2) ok = ok && wait_warp(kVEmpty + st, ((tile >> 1) - 1) & 1);
             if (!ok) break;
-            convert(smem + S::codes + kPos * D, smem + S::v + st * S::kTile, lim);
+            // values behind the sequence's end are zeros, whatever is there: a weight of 0 times NaN is NaN
+            if (lim < kPos) convert(smem + S::codes + kPos * D, smem + S::v + st * S::kTile, true, lim);
+            else convert(smem + S::codes + kPos * D, smem + S::v + st * S::kTile, false, 0);
             tc::fence_proxy_async_smem();
             tc::mbar_arrive(bars + kLEmpty + 1);
             tc::mbar_arrive(bars + kVFull + st);
@@ -607,9 +613,11 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv8_prefill(const __grid_consta
             // ------------------------------------------------------------ pages, scales and the codes' loads
             const int box = p.c.bs() < kPos ? p.c.bs() : kPos, boxes = kPos / box;
             uint32_t issued = 0, steps = (uint32_t)(u1 - u0);
-            int phys = -1, lim = 0, h = 0;
+            int phys = -1, lim = 0, h = 0, e0 = 0;
+            bool fresh = true, item_ends = true;    // the tile is the first of its item in this piece
             auto look = [&](bool there) {    // lane x < 8: the block of positions 16 x .. of the tile at `cur`
                 phys = -1;
+                fresh = item_ends;
                 if (!there) return;
                 const int t0 = cur.lo + cur.step * kPos;
                 lim = cur.L - t0;
@@ -618,12 +626,14 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv8_prefill(const __grid_consta
                     phys = kv8_block(p.c, cur.b, (t0 + lane * 16) >> p.c.bs_log2);
                     if (phys < 0) flag(p.a.status, kStatusBounds);
                 }
-                if (++cur.step >= cur.steps) line.next_item(cur);
+                item_ends = ++cur.step >= cur.steps;
+                if (item_ends) line.next_item(cur);
             };
             bool ok = true;
             if (steps) look(true);
             for (uint32_t tile = 0; tile < steps; ++tile) {
                 const int now = phys, now_h = h, now_lim = lim;
+                const bool first = fresh;
                 look(tile + 1 < steps);
                 float ks = 1.0f, vs = 1.0f;
                 if (now >= 0) {
@@ -631,6 +641,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv8_prefill(const __grid_consta
                     ks = __ldg(p.c.k_scale + unit);
                     vs = __ldg(p.c.v_scale + unit);
                 }
+                if (first) e0 = sum_scale(__shfl_sync(0xFFFFFFFFu, vs, 0));
                 // lane x < boxes copies box x: the block of its first 16 positions
                 const int mine = __shfl_sync(0xFFFFFFFFu, now, (lane * (box / 16)) & 7);
                 const bool copy = lane < boxes && mine >= 0;
@@ -641,7 +652,14 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv8_prefill(const __grid_consta
                     if (tile >= 1) ok = wait_warp(kLEmpty + kv, (tile - 1) & 1);
                     if (!ok) break;
                     if (kv == 0) {
-                        if (lane < 8) sc[(tile & 7) * 8 + lane] = make_float2(ks, (float)((int)(__float_as_uint(vs) >> 23) - 127));
+                        // a block of zero values has the least scale: any will do, and the sums' own is exact
+                        int ev = (int)(__float_as_uint(vs) >> 23) - 127;
+                        if (ev == -120) ev = e0;
+                        const int de = e0 - ev;
+                        if (lane < 8) {
+                            sc[(tile & 7) * 8 + lane] = make_float2(ks, (float)ev);
+                            sg[(tile & 7) * 8 + lane] = exp2_int(de < -126 ? -126 : (de > 126 ? 126 : de));
+                        }
                         if (lane == 0) lims[tile & 7] = now_lim;
                         __syncwarp();
                     }
@@ -669,17 +687,25 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv8_prefill(const __grid_consta
             uint32_t tile = 0, q_phase = 0, p_phase = 0;
             bool ok = true;
             auto scores = [&](int t, int q, uint32_t st) {      // S_t = Q_q K^T
+                const uint64_t a = tc::desc_at(dq, q * S::kTile), b = tc::desc_at(dk, st * S::kTile);
+#pragma unroll 1
+                for (int x = 0; x < S::kPanels; ++x) {
 #pragma unroll
-                for (int x = 0; x < D / 16; ++x) {
-                    const uint32_t off = (x >> 2) * S::kPanel + (x & 3) * 32;
-                    tc::mma_f16(tmem0 + t * 128, tc::desc_at(dq, q * S::kTile + off), tc::desc_at(dk, st * S::kTile + off), idesc_s, x > 0);
+                    for (int y = 0; y < 4; ++y) {
+                        const uint32_t off = x * S::kPanel + y * 32;
+                        tc::mma_f16(tmem0 + t * 128, tc::desc_at(a, off), tc::desc_at(b, off), idesc_s, x + y > 0);
+                    }
                 }
             };
             auto outputs = [&](int t, uint32_t st, bool more) {   // O_t += P_t V
+                const uint64_t b = tc::desc_at(dv, st * S::kTile);
+#pragma unroll 1
+                for (int x = 0; x < 2; ++x) {
 #pragma unroll
-                for (int x = 0; x < kPos / 16; ++x)
-                    tc::mma_f16_ta(tmem0 + kColO + t * D, tmem0 + t * 128 + x * 8, tc::desc_at(dv, st * S::kTile + x * 2048), idesc_o,
-                                   more || x > 0);
+                    for (int y = 0; y < 4; ++y)
+                        tc::mma_f16_ta(tmem0 + kColO + t * D, tmem0 + t * 128 + x * 32 + y * 8, tc::desc_at(b, (x * 4 + y) * 2048),
+                                       idesc_o, more || x + y > 0);
+                }
             };
             int pair = cur.pair, head = cur.h, step = cur.step, todo_all = (int)(u1 - u0);
             while (todo_all > 0 && ok) {
