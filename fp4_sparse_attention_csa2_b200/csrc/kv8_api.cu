@@ -59,7 +59,7 @@ struct Layout {
 
 bool make_layout(const csa2_kv8_cache* c, int T, int H, int n_sel, Layout* L) {
     if (check_cache(c) != CSA2_OK || T < 1 || H < 1 || H % c->n_kv_heads || n_sel < 0) return false;
-    if ((int64_t)T * H >= kMaxRows || (int64_t)c->batch * T * c->n_kv_heads >= kMaxRows) return false;
+    if ((int64_t)T * H >= kMaxRows || (int64_t)c->batch * T * H >= kMaxRows) return false;
     size_t off = 256;
     L->part = off;
     const bool wide = (int64_t)T * (H / c->n_kv_heads) > kKv8StreamRows;
@@ -164,6 +164,7 @@ csa2_status csa2_kv8_attn(const csa2_kv8_cache* cache, const void* q, csa2_dtype
     const csa2_status s = check_query(cache, q, q_dtype, stride_b, stride_t, T, H, n_q, 0, ws, ws_bytes, &k, &L);
     if (s != CSA2_OK) return s;
     if (!out || !aligned(out, 16) || !aligned(lse, 4) || window < 0) return CSA2_ERR_INVALID_ARG;
+    if (window >= (int64_t)cache->max_blocks * cache->block_size) window = 0;   // no position is outside it
     return attention(cache, k, nullptr, 0, window, sm_scale, out, lse, ws, L, stream);
 }
 

@@ -317,6 +317,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv8_prefill(const __grid_consta
                 e0 = (float)sum_scale(vs0);
                 const int j = (cur.row0 + row) / G, g = cur.row0 + row - j * G;
                 pos = mine ? cur.L - cur.n + j : -1;
+                pos = pos < -1 ? -1 : pos;     // before the sequence: nothing is seen either way
                 first = p.a.window ? pos - p.a.window + 1 : 0;
                 // as seen from this half's first column of the item's first step
                 pos -= cur.lo + cur.step * kPos + half * 64;

@@ -269,7 +269,7 @@ __global__ void __launch_bounds__(kThreads, kPerSm) k_kv8_score(const __grid_con
         if (++row >= seq.n * heads) {
             row = 0;
             do seq = sequence(++b, nullptr);
-            while (b < nb && seq.n * seq.tiles == 0);
+            while (b < nb && (seq.n == 0 || seq.tiles == 0));
         }
     }
 }

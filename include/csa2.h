@@ -534,7 +534,8 @@ CSA2_API csa2_status csa2_lse_merge(int R, int batch, int H, int dim, const floa
  *
  * Query row j of sequence b sits at position p = seq_lens[b] - n[b] + j and
  * sees positions t <= p.  H query heads, a multiple of n_kv_heads: head h reads
- * key head h / (H / n_kv_heads).
+ * key head h / (H / n_kv_heads); batch * T * H < 2^31.  Outputs must not overlap
+ * inputs.
  */
 typedef struct {
     uint8_t* k_codes;

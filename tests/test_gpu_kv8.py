@@ -277,6 +277,52 @@ def test_attn_magnitudes(q_scale, spread):
     attend(dev, r, lens, 1, 16, q_scale=q_scale, sm=2.0 ** -20 if q_scale > 8 else None)
 
 
+def test_attn_contiguous_cache_without_bounds_and_a_window_beyond_it():
+    lens, D = [200, 77], 128
+    dev = csa2.KV8Cache(2, 2, D, 5, [0, 0], block_size=64, bounds=False)
+    r = ref.Cache(2, 2, D, 5, 64, 10, None)
+    x = [torch.randn(2, 200, 2, D, generator=torch.Generator().manual_seed(i)).bfloat16() for i in range(2)]
+    csa2.kv8_append(dev, x[0].cuda(), x[1].cuda(), i32([0, 0]), n_new=i32(lens))
+    for b in range(2):
+        r.append(b, 0, x[0][b, :lens[b]].double().numpy(), x[1][b, :lens[b]].double().numpy())
+    dev.seq_lens.copy_(i32(lens))
+    for T in (1, 20):
+        for window in (0, 320, 2 ** 31 - 1):
+            attend(dev, r, lens, T, 8, window=window)
+    idx = torch.zeros(2, 1, 2, 4, dtype=torch.int32, device="cuda")
+    with pytest.raises(csa2.CSA2Error):
+        csa2.kv8_select_blocks(dev, x[0][:, :1].repeat(1, 1, 4, 1).cuda(), idx, workspace(dev, 1, 8, 4))
+
+
+@pytest.mark.parametrize("T", [1, 12])
+def test_many_sequences(T):
+    # more sequences than a warp has lanes, some of them empty: every call's split of the batch
+    rng = np.random.default_rng(T)
+    lens = [int(x) for x in rng.integers(T, 90, 75)]
+    for b in (0, 31, 32, 74):
+        lens[b] = T
+    dev, r = both_caches(75, 2, 64, 16, 7)
+    fill(dev, r, lens)
+    n = [int(x) for x in rng.integers(0, T + 1, 75)]
+    n[1], n[2] = T, 0
+    attend(dev, r, lens, T, 8, n=n)
+    q = torch.randn(75, T, 8, 64, generator=torch.Generator().manual_seed(8)).half().cuda()
+    idx = torch.full((75, T, 2, 3), -7, dtype=torch.int32, device="cuda")
+    ws = workspace(dev, T, 8, 3)
+    out, lse = torch.zeros_like(q), torch.zeros(75, T, 8, device="cuda")
+    csa2.kv8_select_blocks(dev, q, idx, ws, n_first=1, n_q=i32(n))
+    check_select(r, q, idx, lens, n, 1, 1)
+    csa2.kv8_block_attn(dev, q, idx, out, ws, lse=lse, n_q=i32(n))
+    assert csa2.read_device_status(ws) == csa2.OK
+    chosen = idx.cpu().numpy()
+
+    def visible(b, j, h, p):
+        c = chosen[b, j, h]
+        t = (c[c >= 0][:, None] * 16 + np.arange(16)).reshape(-1)
+        return t[t <= p]
+    check_attn(dev, r, q, out, lse, n, 1 / 8, visible, lens)
+
+
 def test_attn_strided_query_and_no_lse():
     lens, H, heads, D = [100, 60], 4, 2, 64
     dev, r = both_caches(2, heads, D, 16, 8)

@@ -111,6 +111,13 @@ def test_selection_needs_bounds_and_a_list_needs_entries(lib):
                                        0x8000, 1 << 40, None) == csa2.ERR_INVALID_ARG
 
 
+def test_row_counts_are_bounded(lib):
+    # batch * T * H of 2^31 rows and more are refused
+    c = ctypes.byref(fake(batch=2048, n_blocks=1 << 12))
+    assert lib.csa2_kv8_workspace_bytes(c, 1 << 15, 32, 0) == 0
+    assert lib.csa2_kv8_workspace_bytes(c, 1 << 14, 32, 0) > 0
+
+
 def test_workspace_grows_with_the_selection(lib):
     c = ctypes.byref(fake())
     plain, chosen = lib.csa2_kv8_workspace_bytes(c, 1, 32, 0), lib.csa2_kv8_workspace_bytes(c, 1, 32, 16)
