@@ -19,7 +19,10 @@ namespace csa2 {
 namespace {
 
 constexpr int kWarps = 4, kThreads = kWarps * 32;
-constexpr int kPerSm = 5;                          // CTAs an SM: 4, 6, 8 are slower (22.4 us; 23.7, 22.7, 24.6 for 32 sequences)
+constexpr int kSlots = 5, kRowBytes = 16 * 128, kSlot = kRowBytes + 128;   // a warp's ring: lines of 16 blocks, their scales and pages
+// CTAs an SM.  5 with four slots: 20.2 against 19.7 us (16,384 blocks of one sequence), 20.1
+// against 18.7 us (32 sequences); 3, or 80 registers a thread, cost 3 us.
+constexpr int kPerSm = 4;
 
 struct Params {
     DevKv8 c;
@@ -108,12 +111,19 @@ struct QueryRows {
     }
 };
 
-// 32 bytes, so that the four lanes of a block's row ask for whole 128-byte lines.
-__device__ __forceinline__ void load32(uint32_t (&w)[8], const uint8_t* p) {
-    asm volatile("ld.global.nc.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
-                 : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]), "=r"(w[4]), "=r"(w[5]), "=r"(w[6]), "=r"(w[7])
-                 : "l"(p));
+// Asynchronous copies of 16 (4) bytes; zeros where `there` is false.
+__device__ __forceinline__ void copy16(void* dst, const void* src, bool there) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"((uint32_t)__cvta_generic_to_shared(dst)), "l"(src),
+                 "r"(there ? 16 : 0) : "memory");
 }
+__device__ __forceinline__ void copy4(void* dst, const void* src, bool there) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"((uint32_t)__cvta_generic_to_shared(dst)), "l"(src),
+                 "r"(there ? 4 : 0) : "memory");
+}
+__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copies_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
+__device__ __forceinline__ uint32_t word(const uint4& v, int i) { return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w; }
 
 // Blocks that query row (b, j) sees; false beyond the call's rows.
 __device__ __forceinline__ bool row_of(const Params& p, int b, int j, int& visible, bool report) {
@@ -129,15 +139,18 @@ __device__ __forceinline__ bool row_of(const Params& p, int b, int j, int& visib
 // lengths are on the device: every warp sums them itself), since rows of one
 // batch differ in length and a warp has only a few tiles.  A tile's blocks are the
 // rows of the matrix tile, eight query heads its columns; the 2 D bytes a block
-// come straight from global memory into operand registers, 32 bytes a lane: the
-// four lanes of a block take a whole line, since an SM asks for about 340 lines
-// a microsecond, whatever part of a line it asks for.  The next line's bounds
-// are in flight while one is multiplied, and the loop is short: fetching
-// straight-line code cost more than the data.
+// go by asynchronous copies into a ring of the warp's own, four lines ahead,
+// whole lines at a time: an SM asks for about 340 lines a microsecond, whatever
+// part of a line it asks for.  (Loads to registers, one line ahead: 20.9 against
+// 19.7 us, 22.3 against 18.7 us.)  With the bounds in L2 it takes as long: what
+// bounds it is the instructions of a line, and those before the first, which
+// have to be fetched; hence the short loops.
 template <int D>
 __global__ void __launch_bounds__(kThreads, kPerSm) k_kv8_score(const __grid_constant__ Params p) {
     constexpr int kLines = D / 64;
+    extern __shared__ __align__(16) uint8_t rings[];
     pdl_begin();
+    uint8_t* ring = rings + (threadIdx.x >> 5) * kSlots * kSlot;
     const int lane = threadIdx.x & 31, r = lane >> 2, c = lane & 3;
     const int nb = p.c.batch, per = (nb + 31) >> 5, heads = p.c.heads;
     struct Seq {
@@ -195,74 +208,90 @@ __global__ void __launch_bounds__(kThreads, kPerSm) k_kv8_score(const __grid_con
         const int j = row / heads, h = row - j * heads;
         const int nt = seq.tiles - t0 < u1 - u ? seq.tiles - t0 : (int)(u1 - u), first = t0 * 16;
         const int pos = seq.L - seq.n + j, visible = pos < 0 ? 0 : (pos >> p.c.bs_log2) + 1;
-        auto page = [&](int t, int half) {      // physical block of block r (+ 8) of tile t
-            const int lb = first + t * 16 + half * 8 + r;
-            return t < nt && lb < visible ? kv8_block(p.c, b, lb) : -1;
+        // pages of tiles t and t + 1: lanes 0 .. 15 and 16 .. 31
+        auto pages = [&](int t) {
+            const int lb = first + t * 16 + lane;
+            return t + (lane >> 4) < nt && lb < visible ? kv8_block(p.c, b, lb) : -1;
         };
-        auto load = [&](uint32_t (&w)[2][8], const int (&phys)[2], int x) {
-#pragma unroll
-            for (int half = 0; half < 2; ++half) {
-#pragma unroll
-                for (int i = 0; i < 8; ++i) w[half][i] = 0;
-                if (phys[half] >= 0)
-                    load32(w[half], p.c.k_bounds + ((int64_t)phys[half] * heads + h) * 2 * D + x * 128 + c * 32);
-            }
-        };
+        const uint8_t* base = p.c.k_bounds + h * 2 * D + (lane & 7) * 16;
         float* out = p.scores + ((int64_t)(b * p.q.T + j) * heads + h) * p.c.max_blocks;
         for (int g0 = 0; g0 < p.G && first < visible; g0 += 8) {
-            int here[2] = {page(0, 0), page(0, 1)}, next[2] = {page(1, 0), page(1, 1)};
+            int now = pages(0), next = pages(2), sent = 0, to = 0;   // line `sent` goes to slot `to` next
+            auto send = [&] {
+                const int t = sent / kLines, x = sent - t * kLines;
+                uint8_t* slot = ring + to * kSlot;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int row = i * 4 + (lane >> 3), phys = __shfl_sync(0xFFFFFFFFu, now, (t & 1) * 16 + row);
+                    copy16(slot + row * 128 + (((lane & 7) ^ (row & 7)) << 4),
+                           base + (int64_t)(phys < 0 ? 0 : phys) * heads * 2 * D + x * 128, phys >= 0);
+                }
+                if (x == kLines - 1) {       // the tile's pages and key scales, with its last line
+                    const int phys = __shfl_sync(0xFFFFFFFFu, now, (t & 1) * 16 + (lane & 15));
+                    if (lane < 16) {
+                        copy4(slot + kRowBytes + lane * 4, p.c.k_scale + (int64_t)(phys < 0 ? 0 : phys) * heads + h, phys >= 0);
+                        reinterpret_cast<int*>(slot + kRowBytes + 64)[lane] = phys;
+                    }
+                    if (t & 1) {
+                        now = next;
+                        next = pages(t + 3);
+                    }
+                }
+                ++sent;
+                if (++to == kSlots) to = 0;
+            };
             QueryRows<D> q;
             q.load(p, b, j, h, g0, r, c);
-            uint32_t w[2][8], v[2][8];
-            load(w, here, 0);
-            q.round(p, g0, r, c);
-            float acc[4] = {0.0f, 0.0f, 0.0f, 0.0f}, ks[2];
-            int t = 0, x = 0;
+            const int lines = nt * kLines;
 #pragma unroll 1
-            for (;;) {
-                const bool last = x == kLines - 1;      // of the tile
-                load(v, last ? next : here, last ? 0 : 1);
-                if (x == 0) {
-#pragma unroll
-                    for (int half = 0; half < 2; ++half)
-                        ks[half] = here[half] >= 0 ? __ldg(p.c.k_scale + (int64_t)here[half] * heads + h) : 0.0f;
-                }
-#pragma unroll
-                for (int s = 0; s < 8; ++s) {
-                    const uint32_t a[4] = {half2_lo(w[0][s]), half2_lo(w[1][s]), half2_hi(w[0][s]), half2_hi(w[1][s])};
-                    mma_16816(acc, a, q.part(x, 2 * s), q.part(x, 2 * s + 1));
-                }
-                if (last) {
-                    // rows without a query head hold 0 * -inf: fmaxf drops the NaN
-                    float best[2] = {fmaxf(acc[0] * q.unit[0], acc[1] * q.unit[1]), fmaxf(acc[2] * q.unit[0], acc[3] * q.unit[1])};
-#pragma unroll
-                    for (int half = 0; half < 2; ++half) {
-                        best[half] = fmaxf(best[half], __shfl_xor_sync(0xFFFFFFFFu, best[half], 1));
-                        best[half] = fmaxf(best[half], __shfl_xor_sync(0xFFFFFFFFu, best[half], 2));
-                        const int lb = first + t * 16 + half * 8 + r;
-                        if (c == 0 && lb < visible) {
-                            if (here[half] < 0) flag(p.status, kStatusBounds);
-                            const float score = here[half] < 0 ? -INFINITY : best[half] * ks[half];
-                            out[lb] = g0 ? fmaxf(score, out[lb]) : score;
-                        }
-                    }
-                    acc[0] = acc[1] = acc[2] = acc[3] = 0.0f;
-                    ++t;
-                    if (t >= nt || first + t * 16 >= visible) break;
-#pragma unroll
-                    for (int half = 0; half < 2; ++half) {
-                        here[half] = next[half];
-                        next[half] = page(t + 1, half);
-                    }
-                    x = 0;
-                } else {
-                    ++x;
-                }
+            for (int s = 0; s < kSlots - 1; ++s) {
+                if (s < lines) send();
+                copies_commit();
+            }
+            q.round(p, g0, r, c);
+            float acc[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+            int t = 0, x = 0, at = 0;
+#pragma unroll 1
+            for (int s = 0; s < lines; ++s) {
+                copies_wait<kSlots - 2>();
+                __syncwarp();                       // everyone's copies are there, and the slot before has been read
+                if (sent < lines) send();
+                copies_commit();
+                const uint8_t* slot = ring + at * kSlot;
+                uint4 w[2][2];
 #pragma unroll
                 for (int half = 0; half < 2; ++half)
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) w[half][i] = v[half][i];
+                    for (int i = 0; i < 2; ++i)
+                        w[half][i] = *reinterpret_cast<const uint4*>(slot + (half * 8 + r) * 128 + (((2 * c + i) ^ r) << 4));
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const uint32_t u0 = word(w[0][i >> 2], i & 3), u1 = word(w[1][i >> 2], i & 3);
+                    const uint32_t a[4] = {half2_lo(u0), half2_lo(u1), half2_hi(u0), half2_hi(u1)};
+                    mma_16816(acc, a, q.part(x, 2 * i), q.part(x, 2 * i + 1));
+                }
+                if (++at == kSlots) at = 0;
+                if (++x < kLines) continue;
+                x = 0;
+                // rows without a query head hold 0 * -inf: fmaxf drops the NaN
+                float best[2] = {fmaxf(acc[0] * q.unit[0], acc[1] * q.unit[1]), fmaxf(acc[2] * q.unit[0], acc[3] * q.unit[1])};
+#pragma unroll
+                for (int half = 0; half < 2; ++half) {
+                    best[half] = fmaxf(best[half], __shfl_xor_sync(0xFFFFFFFFu, best[half], 1));
+                    best[half] = fmaxf(best[half], __shfl_xor_sync(0xFFFFFFFFu, best[half], 2));
+                    const int lb = first + t * 16 + half * 8 + r;
+                    if (c == 0 && lb < visible) {
+                        const bool here = reinterpret_cast<const int*>(slot + kRowBytes + 64)[half * 8 + r] >= 0;
+                        if (!here) flag(p.status, kStatusBounds);
+                        const float score = here ? best[half] * reinterpret_cast<const float*>(slot + kRowBytes)[half * 8 + r] : -INFINITY;
+                        out[lb] = g0 ? fmaxf(score, out[lb]) : score;
+                    }
+                }
+                acc[0] = acc[1] = acc[2] = acc[3] = 0.0f;
+                ++t;
             }
+            copies_wait<0>();
+            __syncwarp();                           // the ring is free
         }
         u += nt;
         t0 = 0;
@@ -500,8 +529,9 @@ cudaError_t launch_kv8_select(const DevKv8& c, const Kv8Query& q, int n_sel, int
     if (e != cudaSuccess) return e;
     const int64_t most = ((int64_t)rows * ((c.max_blocks + 15) / 16) + kWarps - 1) / kWarps;   // CTAs with a tile a warp
     const unsigned ctas = (unsigned)(most < sms * kPerSm ? most : sms * kPerSm);
-    e = c.dim == 64 ? launch_pdl(k_kv8_score<64>, ctas, kThreads, 0, st, p)
-                    : launch_pdl(k_kv8_score<128>, ctas, kThreads, 0, st, p);
+    const int ring = kWarps * kSlots * kSlot;
+    e = c.dim == 64 ? launch_pdl(k_kv8_score<64>, ctas, kThreads, ring, st, p)
+                    : launch_pdl(k_kv8_score<128>, ctas, kThreads, ring, st, p);
     if (e != cudaSuccess) return e;
     const auto select = c.max_blocks <= 2 * kSelThreads    ? k_kv8_select<2>
                         : c.max_blocks <= 8 * kSelThreads  ? k_kv8_select<8>
