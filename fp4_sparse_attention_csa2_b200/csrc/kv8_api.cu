@@ -109,9 +109,9 @@ csa2_status attention(const csa2_kv8_cache* c, const Kv8Query& q, const int32_t*
     a.lse = lse;
     a.part = at<float>(ws, L.part);
     a.status = at<uint32_t>(ws, 0);
-    const bool wide = !block_idx && (int64_t)q.T * (q.H / c->n_kv_heads) > kKv8StreamRows;
+    const DevKv8 d = dev_kv8(c);
     const cudaStream_t st = static_cast<cudaStream_t>(stream);
-    return cuda_status(wide ? launch_kv8_prefill(dev_kv8(c), a, st) : launch_kv8_attn(dev_kv8(c), a, st));
+    return cuda_status(kv8_streams(d, a) ? launch_kv8_attn(d, a, st) : launch_kv8_prefill(d, a, st));
 }
 
 }  // namespace

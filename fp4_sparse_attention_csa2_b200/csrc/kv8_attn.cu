@@ -60,6 +60,8 @@ constexpr float kHeadroom = 8.0f;
 // with two stages take 117 against 112 us for 32 sequences of up to 16,384 tokens.
 constexpr int kPerSm = 2;
 constexpr int kMaxCtas = kPerSm * 148;
+constexpr int kMergeWarps = 16;           // of a CTA of k_kv8_combine_few
+constexpr int kFewItems = 16, kFewSteps = 16;   // it merges where an item can have as many pieces, and as many steps
 
 struct Params {
     DevKv8 c;
@@ -925,6 +927,106 @@ __global__ void __launch_bounds__(4 * D) k_kv8_combine(const __grid_constant__ P
     if (p.a.lse && q4 == 0) p.a.lse[at] = l == 0.0f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
 }
 
+// The same for few items, each in many pieces: blockIdx.x counts the items that
+// were cut, a CTA merges one row, warp w the parts w, w + 16, .. in this order, the
+// first warp the sixteen.  With k_kv8_combine two heads of 24,415 positions, 148
+// parts each, take 27.7 us, with this 14.5; 8 heads of a million positions 173.1
+// and 168.9; two heads of 64 blocks (32 parts) 11.3 and 9.9; but four heads of
+// 1,000 positions (8 parts) 8.4 and 9.1.
+template <int D, int NT, bool LIST>
+__global__ void __launch_bounds__(kMergeWarps * 32) k_kv8_combine_few(const __grid_constant__ Params p) {
+    constexpr int kLanes = D / 4, kAtOnce = 32 / kLanes;     // lanes of a part's row, parts a warp reads at once
+    static_assert(kMaxCtas <= kMergeWarps * 32, "a thread a piece, a lane a part");
+    __shared__ float4 acc[kMergeWarps][kLanes];
+    __shared__ float stat[kMergeWarps][3];
+    __shared__ int starts[kMergeWarps], found[6];
+    pdl_begin();
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    int parts = 0;                                           // a thread a piece
+    int4 item = make_int4(0, 0, 0, 0);                       // b, h, rt, rows
+    if (tid < p.ctas) {
+        const float* d = p.a.part + ((int64_t)tid * 2 + 1) * Part<D>::kFloats + Part<D>::kDesc;
+        item = *reinterpret_cast<const int4*>(d);
+        parts = reinterpret_cast<const int*>(d)[4];
+    }
+    const uint32_t cut = __ballot_sync(0xFFFFFFFFu, parts >= 2);
+    if (lane == 0) starts[warp] = __popc(cut);
+    if (tid == 0) found[0] = -1;
+    __syncthreads();
+    const int before = __reduce_add_sync(0xFFFFFFFFu, lane < warp ? starts[lane] : 0) + __popc(cut & ((1u << lane) - 1));
+    if (parts >= 2 && before == (int)blockIdx.x) {
+        found[0] = tid, found[1] = parts;
+        found[2] = item.x, found[3] = item.y, found[4] = item.z, found[5] = item.w;
+    }
+    __syncthreads();
+    const int x = found[0], row = blockIdx.y;
+    if (x < 0 || row >= found[5]) return;
+    parts = found[1];
+    const int q4 = lane % kLanes;
+    auto part = [&](int i) { return p.a.part + ((int64_t)(x + i) * 2 + (i == 0 ? 1 : 0)) * Part<D>::kFloats; };
+    const int n = warp < parts ? (parts - warp - 1) / kMergeWarps + 1 : 0;    // this warp's, a lane each
+    float pl = 0.0f, pm = kNone, pM = kNone;
+    if (lane < n) {
+        const float* s3 = part(warp + lane * kMergeWarps) + Part<D>::kStats + row * 3;
+        pm = s3[0], pl = s3[1], pM = s3[2];
+    }
+    float m = pm, M = pM;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+        m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
+        M = fmaxf(M, __shfl_xor_sync(0xFFFFFFFFu, M, o));
+    }
+    float l = pl * ex2(pm - m);
+    const float f = ex2(pM - M);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xFFFFFFFFu, l, o);
+    float4 s = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll 8
+    for (int k = 0; k < n; k += kAtOnce) {
+        const int at = k + lane / kLanes;
+        const float w = __shfl_sync(0xFFFFFFFFu, f, at & 31);
+        if (at < n) {
+            const float4 v = *reinterpret_cast<const float4*>(part(warp + at * kMergeWarps) + row * D + q4 * 4);
+            s.x += v.x * w;
+            s.y += v.y * w;
+            s.z += v.z * w;
+            s.w += v.w * w;
+        }
+    }
+    if (kAtOnce == 2) {
+        s.x += __shfl_xor_sync(0xFFFFFFFFu, s.x, 16);
+        s.y += __shfl_xor_sync(0xFFFFFFFFu, s.y, 16);
+        s.z += __shfl_xor_sync(0xFFFFFFFFu, s.z, 16);
+        s.w += __shfl_xor_sync(0xFFFFFFFFu, s.w, 16);
+    }
+    if (lane < kLanes) acc[warp][q4] = s;
+    if (lane == 0) stat[warp][0] = m, stat[warp][1] = l, stat[warp][2] = M;
+    __syncthreads();
+    if (warp || lane >= kLanes) return;
+    for (int i = 1; i < kMergeWarps; ++i) {
+        m = fmaxf(m, stat[i][0]);
+        M = fmaxf(M, stat[i][2]);
+    }
+    float y[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+    l = 0.0f;
+    for (int i = 0; i < kMergeWarps; ++i) {
+        const float4 v = acc[i][q4];
+        const float f = ex2(stat[i][2] - M);
+        l += stat[i][1] * ex2(stat[i][0] - m);
+        y[0] += v.x * f;
+        y[1] += v.y * f;
+        y[2] += v.z * f;
+        y[3] += v.w * f;
+    }
+    const Work<NT, LIST> work(p);
+    Cursor k;
+    k.rt = found[4];
+    const int2 jg = work.token(k, row);
+    const int64_t at = ((int64_t)found[2] * p.a.q.T + jg.x) * p.a.q.H + found[3] * p.G + jg.y;
+    store_out(p.a.out, p.a.q.is_bf16, at * D + q4 * 4, y, l == 0.0f ? 0.0f : ex2(M - m - kHeadroom) / l);
+    if (p.a.lse && q4 == 0) p.a.lse[at] = l == 0.0f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
+}
+
 template <int D, int NT, bool LIST>
 cudaError_t launch(Params& p, cudaStream_t st) {
     using S = Smem<D, NT>;
@@ -944,6 +1046,14 @@ cudaError_t launch(Params& p, cudaStream_t st) {
     if (e != cudaSuccess) return e;
     const int64_t rows = LIST ? p.G : (int64_t)p.a.q.T * p.G;
     const int most = rows < 8 * NT ? (int)rows : 8 * NT;
+    // items that can be cut: no more than there are, and than there are pieces
+    const int64_t tiles = LIST ? (int64_t)p.a.q.T * p.gt : (rows + 8 * NT - 1) / (8 * NT);
+    const int64_t items = (int64_t)p.c.batch * p.c.heads * tiles;
+    // pieces an item can be in: no more than its steps
+    const int64_t span = LIST ? (int64_t)p.a.n_sel << p.c.bs_log2 : (int64_t)p.c.max_blocks << p.c.bs_log2;
+    const int64_t seen = !LIST && p.a.window && (int64_t)p.a.window + p.a.q.T < span ? (int64_t)p.a.window + p.a.q.T : span;
+    if (items * kFewItems <= p.ctas && seen >= kFewSteps * kStep)
+        return launch_pdl(k_kv8_combine_few<D, NT, LIST>, dim3((unsigned)items, most), kMergeWarps * 32, 0, st, p);
     return launch_pdl(k_kv8_combine<D, NT, LIST>, dim3(p.ctas, (most + 3) / 4), 4 * D, 0, st, p);
 }
 

@@ -44,6 +44,7 @@ constexpr int kRows = 256, kTileRows = 128, kPos = 128;
 constexpr int kThreads = 768, kConv = 128, kSoftmax = 512;   // all, converter's, softmax's
 constexpr int kMaxCtas = 148;
 constexpr int kMmaWarp = 20, kLoadWarp = 21;
+constexpr int kMergeWarps = 16, kFewItems = 16;   // of a CTA of k_kv8_prefill_combine_few; pieces an item from which it merges
 constexpr float kNone = -3.0e38f;
 constexpr float kHeadroom = 8.0f;   // weights are 2^(z - M + 8): full fp16 precision down to 2^-22
 constexpr float kLazy = 7.0f;       // and at most 2^15 (fp16: 65504) before the maximum is moved
@@ -802,6 +803,26 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv8_prefill(const __grid_consta
     if (warp == kMmaWarp) tc::tmem_dealloc(tmem, 512);
 }
 
+// Four channels of a merged row, and its logarithm of the sum.
+template <int D>
+__device__ __forceinline__ void store_row(const Params& p, int b, int h, int row, int q4, const float4& s, float m, float M, float l) {
+    const int j = row / p.G, g = row - j * p.G;
+    const int64_t at = ((int64_t)b * p.a.q.T + j) * p.a.q.H + h * p.G + g;
+    const float f = l == 0.0f ? 0.0f : ex2(M - m) / l;
+    uint32_t w[2];
+    if (p.a.q.is_bf16) {
+        const __nv_bfloat162 a = __floats2bfloat162_rn(s.x * f, s.y * f), b2 = __floats2bfloat162_rn(s.z * f, s.w * f);
+        memcpy(&w[0], &a, 4);
+        memcpy(&w[1], &b2, 4);
+    } else {
+        const __half2 a = __floats2half2_rn(s.x * f, s.y * f), b2 = __floats2half2_rn(s.z * f, s.w * f);
+        memcpy(&w[0], &a, 4);
+        memcpy(&w[1], &b2, 4);
+    }
+    *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.a.out) + at * D + q4 * 4) = make_uint2(w[0], w[1]);
+    if (p.a.lse && q4 == 0) p.a.lse[at] = l == 0.0f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
+}
+
 // The items that the line's cuts went through: CTA x merges the item that
 // starts in piece x, 16 bytes of a row a thread, the parts in order.
 template <int D>
@@ -831,21 +852,81 @@ __global__ void __launch_bounds__(256) k_kv8_prefill_combine(const __grid_consta
         s.z += v.z * f;
         s.w += v.w * f;
     }
-    const int j = (desc[2] + row) / p.G, g = desc[2] + row - j * p.G;
-    const int64_t at = ((int64_t)desc[0] * p.a.q.T + j) * p.a.q.H + desc[1] * p.G + g;
-    const float f = l == 0.0f ? 0.0f : ex2(M - m) / l;
-    uint32_t w[2];
-    if (p.a.q.is_bf16) {
-        const __nv_bfloat162 a = __floats2bfloat162_rn(s.x * f, s.y * f), b = __floats2bfloat162_rn(s.z * f, s.w * f);
-        memcpy(&w[0], &a, 4);
-        memcpy(&w[1], &b, 4);
-    } else {
-        const __half2 a = __floats2half2_rn(s.x * f, s.y * f), b = __floats2half2_rn(s.z * f, s.w * f);
-        memcpy(&w[0], &a, 4);
-        memcpy(&w[1], &b, 4);
+    store_row<D>(p, desc[0], desc[1], desc[2] + row, q4, s, m, M, l);
+}
+
+// The same for few items, each in many pieces: blockIdx.x counts the items that
+// were cut; a lane is a row, warp w takes the parts w, w + 16, .. in this order
+// and the first warp adds the sixteen up.  One head with 32 rows over 24,415
+// positions, 148 parts: 67.2 us with the kernel above, 23.0 with this; with 256
+// rows over 131,072 positions 93.7 and 44.5.
+template <int D>
+__global__ void __launch_bounds__(kMergeWarps * 32) k_kv8_prefill_combine_few(const __grid_constant__ Params p) {
+    static_assert(kMaxCtas <= kMergeWarps * 32, "a thread a piece");
+    __shared__ float4 acc[kMergeWarps][32];
+    __shared__ float stat[kMergeWarps][3][32];
+    __shared__ int starts[kMergeWarps], found[2];
+    pdl_begin();
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, q4 = blockIdx.y;
+    auto desc = [&](int x) {
+        return reinterpret_cast<const int*>(p.a.part + ((int64_t)x * 2 + 1) * Part<D>::kFloats + Part<D>::kDesc);
+    };
+    const int own = tid < p.ctas ? desc(tid)[4] : 0;
+    const uint32_t cut = __ballot_sync(0xFFFFFFFFu, own >= 2);
+    if (lane == 0) starts[warp] = __popc(cut);
+    if (tid == 0) found[0] = -1;
+    __syncthreads();
+    const int before = __reduce_add_sync(0xFFFFFFFFu, lane < warp ? starts[lane] : 0) + __popc(cut & ((1u << lane) - 1));
+    if (own >= 2 && before == (int)blockIdx.x) found[0] = tid, found[1] = own;
+    __syncthreads();
+    const int x = found[0], parts = found[1];
+    if (x < 0) return;
+    const int* item = desc(x);
+    const int rows = item[3], row = blockIdx.z * 32 + lane;
+    if ((int)blockIdx.z * 32 >= rows) return;
+    auto part = [&](int i) { return p.a.part + ((int64_t)(x + i) * 2 + (i == 0 ? 1 : 0)) * Part<D>::kFloats; };
+    float m = kNone, M = kNone, l = 0.0f;
+    float4 s = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    if (row < rows) {
+#pragma unroll 8
+        for (int i = warp; i < parts; i += kMergeWarps) {
+            const float* s3 = part(i) + Part<D>::kStats + row * 3;
+            m = fmaxf(m, s3[0]);
+            M = fmaxf(M, s3[2]);
+        }
+#pragma unroll 4
+        for (int i = warp; i < parts; i += kMergeWarps) {
+            const float* b = part(i);
+            const float* s3 = b + Part<D>::kStats + row * 3;
+            const float4 v = reinterpret_cast<const float4*>(b)[(int64_t)q4 * kRows + row];
+            l += s3[1] * ex2(s3[0] - m);
+            const float f = ex2(s3[2] - M);
+            s.x += v.x * f;
+            s.y += v.y * f;
+            s.z += v.z * f;
+            s.w += v.w * f;
+        }
     }
-    *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.a.out) + at * D + q4 * 4) = make_uint2(w[0], w[1]);
-    if (p.a.lse && q4 == 0) p.a.lse[at] = l == 0.0f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
+    acc[warp][lane] = s;
+    stat[warp][0][lane] = m, stat[warp][1][lane] = l, stat[warp][2][lane] = M;
+    __syncthreads();
+    if (warp || row >= rows) return;
+    for (int i = 1; i < kMergeWarps; ++i) {
+        m = fmaxf(m, stat[i][0][lane]);
+        M = fmaxf(M, stat[i][2][lane]);
+    }
+    l = 0.0f;
+    s = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    for (int i = 0; i < kMergeWarps; ++i) {
+        const float4 v = acc[i][lane];
+        l += stat[i][1][lane] * ex2(stat[i][0][lane] - m);
+        const float f = ex2(stat[i][2][lane] - M);
+        s.x += v.x * f;
+        s.y += v.y * f;
+        s.z += v.z * f;
+        s.w += v.w * f;
+    }
+    store_row<D>(p, item[0], item[1], item[2] + row, q4, s, m, M, l);
 }
 
 template <int D>
@@ -859,6 +940,12 @@ cudaError_t launch(const Params& p, cudaStream_t st) {
     if (!kv8_row_map(&kmap, p.c, p.c.k, box, false) || !kv8_row_map(&vmap, p.c, p.c.v, box, false)) return cudaErrorNotSupported;
     e = launch_pdl(k_kv8_prefill<D>, p.ctas, kThreads, S::bytes, st, p, kmap, vmap);
     if (e != cudaSuccess) return e;
+    const int64_t items = (int64_t)p.c.batch * p.c.heads * p.row_blocks;
+    if (items * kFewItems <= p.ctas) {
+        const int64_t rows = (int64_t)p.a.q.T * p.G;
+        return launch_pdl(k_kv8_prefill_combine_few<D>, dim3((unsigned)items, D / 4, (unsigned)((rows < kRows ? rows : kRows) + 31) / 32),
+                          kMergeWarps * 32, 0, st, p);
+    }
     return launch_pdl(k_kv8_prefill_combine<D>, dim3(p.ctas, D / 4), kRows, 0, st, p);
 }
 

@@ -475,6 +475,63 @@ def test_attn_many_rows_wait_that_runs_out():
     assert csa2.read_device_status(ws) == csa2.OK and torch.equal(out, want)
 
 
+# ---------------------------------------------------------------- the same rows of a cache with room for far more
+# positions (the kernel for many rows is chosen by how far the cache reaches, not by the lengths), every table entry
+# behind the sequences outside the cache
+@pytest.fixture
+def with_room(monkeypatch):
+    near = both_caches
+
+    def far(B, heads, D, bs, max_blocks, *args, **kw):
+        dev, r = near(B, heads, D, bs, max_blocks, *args, **kw)
+        table = torch.full((B, (1 << 20) // bs), -1, dtype=torch.int32, device="cuda")
+        table[:, :max_blocks] = dev.block_table
+        return csa2.KV8Cache.wrap(dev.k, dev.v, dev.k_scale, dev.v_scale, dev.seq_lens, dev.k_bounds, table), r
+    monkeypatch.setitem(globals(), "both_caches", far)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+@pytest.mark.parametrize("heads,G,D,bs,lens,T", [
+    (1, 8, 128, 64, [400], 100), (2, 4, 64, 16, [130, 257, 90], 70), (3, 5, 128, 128, [300, 220], 60),
+    (1, 33, 128, 32, [64, 40], 8), (2, 2, 128, 16, [515], 515), (1, 1, 128, 64, [33, 2000], 33),
+    (1, 4, 64, 32, [5000], 9), (1, 16, 128, 64, [6000], 3), (2, 8, 128, 128, [2600], 33),
+])
+def test_attn_many_rows_with_room(with_room, heads, G, D, bs, lens, T, dtype):
+    test_attn_many_rows(heads, G, D, bs, lens, T, 0, dtype)
+
+
+@pytest.mark.parametrize("heads,G,D,bs,lens,T,window", [
+    (2, 8, 128, 64, [400, 257, 350], 256, 129), (2, 16, 64, 32, [300, 280], 255, 33), (1, 16, 128, 16, [900], 500, 200)])
+def test_attn_many_rows_window(with_room, heads, G, D, bs, lens, T, window):
+    test_attn_many_rows(heads, G, D, bs, lens, T, window, "bf16")
+
+
+def test_attn_many_rows_with_room_padded_and_empty(with_room):
+    test_attn_many_rows_padded_and_empty()
+
+
+@pytest.mark.parametrize("q_scale,spread", [(2.0 ** -60, 1.0), (1.0, 7.0), (6.0, 3.0)])
+def test_attn_many_rows_with_room_magnitudes(with_room, q_scale, spread):
+    test_attn_many_rows_magnitudes(q_scale, spread)
+
+
+def test_attn_many_rows_with_room_zero_values(with_room):
+    test_attn_many_rows_zero_values()
+
+
+def test_attn_many_rows_with_room_wait_that_runs_out(with_room):
+    test_attn_many_rows_wait_that_runs_out()
+
+
+@pytest.mark.parametrize("heads,G,D,bs,lens,T,window", [
+    (1, 8, 128, 64, [5000], 1, 0), (2, 3, 64, 16, [4100, 2500], 1, 0), (1, 16, 64, 128, [9000], 2, 0),
+    (3, 5, 128, 32, [2100], 3, 0), (1, 1, 128, 64, [30000, 1], 1, 0), (2, 8, 128, 64, [8000], 1, 3000)])
+def test_attn_few_items_in_many_pieces(heads, G, D, bs, lens, T, window):
+    dev, r = both_caches(len(lens), heads, D, bs, (max(lens) + bs - 1) // bs + 1)
+    fill(dev, r, lens)
+    attend(dev, r, lens, T, heads * G, window=window)
+
+
 def test_offsets_beyond_32_bits():
     # codes of more than 4 GiB a side: the sequence's blocks lie at the far end
     heads, D, bs, mb = 8, 128, 64, 5
