@@ -403,7 +403,9 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv8_prefill(const __grid_consta
                     for (int q = 0; q < 4; ++q) {
                         const uint32_t* v = r + q * 16;
                         const float2 f = f2[q];
-                        const float a = zs * f.x, d = f.y - M + kHeadroom;
+                        // at least the least normal number: 0 times a masked -inf would be NaN, and what is
+                        // added to a logit, |S| < 2^31, is below 2^-95
+                        const float a = fmaxf(zs * f.x, 1.17549435e-38f), d = f.y - M + kHeadroom;
                         const uint64_t ff = pack2(a, a), dd = pack2(d, d);
                         uint64_t sum = 0;
                         float m = __uint_as_float(v[0]);

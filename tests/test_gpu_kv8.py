@@ -523,6 +523,24 @@ def test_attn_many_rows_with_room_wait_that_runs_out(with_room):
     test_attn_many_rows_wait_that_runs_out()
 
 
+@pytest.mark.parametrize("T", [1, 16, 24])
+@pytest.mark.parametrize("q_scale", [0.0, 2.0 ** -40, 2.0 ** -15])
+def test_attn_zero_keys_and_small_queries(with_room, T, q_scale):
+    # the product of the query's and a zero block's scale is below what fp32 holds
+    lens, D = [200, 64], 64
+    dev, r = both_caches(2, 2, D, 64, 5)
+    g = torch.Generator().manual_seed(3)
+    k, v = torch.randn(2, 200, 2, D, generator=g), torch.randn(2, 200, 2, D, generator=g)
+    k[:, :64] = 0
+    k[:, 128:192] = 0
+    csa2.kv8_append(dev, k.cuda(), v.cuda(), i32([0, 0]), n_new=i32(lens))
+    for b in range(2):
+        r.append(b, 0, k[b, :lens[b]].double().numpy(), v[b, :lens[b]].double().numpy())
+    dev.seq_lens.copy_(i32(lens))
+    for dtype in (torch.bfloat16, torch.float16):
+        attend(dev, r, lens, T, 4, q_scale=q_scale, dtype=dtype)
+
+
 @pytest.mark.parametrize("heads,G,D,bs,lens,T,window", [
     (1, 8, 128, 64, [5000], 1, 0), (2, 3, 64, 16, [4100, 2500], 1, 0), (1, 16, 64, 128, [9000], 2, 0),
     (3, 5, 128, 32, [2100], 3, 0), (1, 1, 128, 64, [30000, 1], 1, 0), (2, 8, 128, 64, [8000], 1, 3000)])
