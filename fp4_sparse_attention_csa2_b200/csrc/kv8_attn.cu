@@ -372,8 +372,10 @@ __global__ void __launch_bounds__(kThreads, kPerSm) k_kv8_attn(const __grid_cons
             } else {
                 const int t = at.lo + off;
                 k.row = t & (bs - 1);
-                if (t < at.L) k.lb[0] = t >> p.c.bs_log2;
-                if (pairs && t + kGroup < at.L) k.lb[1] = k.lb[0] + 1;
+                const int lb = t >> p.c.bs_log2;
+                // a block of 16 before every row's window is not looked up: its page may be gone
+                if (t < at.L && !(pairs && p.a.window && t + kGroup <= at.L - at.n - p.a.window + 1)) k.lb[0] = lb;
+                if (pairs && t + kGroup < at.L) k.lb[1] = lb + 1;
             }
             ++ahead_u;
             --todo_left;

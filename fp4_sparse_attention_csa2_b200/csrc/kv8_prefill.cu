@@ -90,6 +90,12 @@ struct Line {
         k.steps = seen > 0 ? (int)((seen + kPos - 1) / kPos) : 1;  // an empty row still has to be written
     }
     __device__ __forceinline__ int64_t total(const Cursor& k) const { return (int64_t)p.c.heads * k.steps; }
+    // Whether position t's block is to be looked up: it holds positions, and not only
+    // such as lie before every row's window (their page may be gone).
+    __device__ __forceinline__ bool seen(const Cursor& k, int t) const {
+        const int64_t first = p.a.window ? (int64_t)k.L - k.n + k.row0 / p.G - p.a.window + 1 : 0;
+        return t < k.L && ((((int64_t)t >> p.c.bs_log2) + 1) << p.c.bs_log2) > first;
+    }
     __device__ __forceinline__ void next_item(Cursor& k) const {
         k.step = 0;
         if (++k.h < p.c.heads) return;
@@ -193,7 +199,7 @@ struct Smem {
     static constexpr int sums = codes;                        // kThreads + 1 words, before the first load
     static constexpr int sc = codes + 2 * kPos * D;           // [8][8] key scale, log2 of the value scale
     static constexpr int sg = sc + 8 * 8 * 8;                 // [8][8] 2^(e0 - that)
-    static constexpr int lims = sg + 8 * 8 * 4;               // [8] positions of a tile before the sequence's end
+    static constexpr int lims = sg + 8 * 8 * 4;               // [8] positions of a tile that are values
     static constexpr int xch = lims + 8 * 4;                  // [tile][half][128] floats: halves of a row agree
     static constexpr int bars = xch + 4 * 128 * 4;
     static constexpr int misc = bars + 20 * 8;                // TMEM base, dead
@@ -313,7 +319,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv8_prefill(const __grid_consta
                 const int row = dual ? rt : t * kTileRows + rt;
                 const bool mine = row < cur.rows;
                 const int at0 = cur.lo + cur.step * kPos;
-                const int block0 = at0 < cur.L ? kv8_block(p.c, cur.b, at0 >> p.c.bs_log2) : -1;
+                const int block0 = line.seen(cur, at0) ? kv8_block(p.c, cur.b, at0 >> p.c.bs_log2) : -1;
                 const float vs0 = block0 >= 0 ? __ldg(p.c.v_scale + (int64_t)block0 * p.c.heads + cur.h) : 1.0f;
                 e0 = (float)sum_scale(vs0);
                 const int j = (cur.row0 + row) / G, g = cur.row0 + row - j * G;
@@ -575,13 +581,13 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv8_prefill(const __grid_consta
         const int ct = tid - kSoftmax, l8 = ct & 7;
         // Piece (16 codes, two 16-byte chunks of fp16) `x` of this thread: eight lanes load 128 dense bytes'
         // worth of distinct banks and store to eight distinct ones.
-        auto convert = [&](const uint8_t* src, uint8_t* dst, bool clear, int lim) {
+        auto convert = [&](const uint8_t* src, uint8_t* dst, bool clear, int lead, int lim) {
 #pragma unroll 4
             for (int x = 0; x < D / 16; ++x) {
                 const int row = D == 128 ? 2 * ((ct >> 3) + 16 * (x >> 1)) + ((l8 >> 2) ^ (x & 1)) : (ct >> 2) + 32 * x;
                 const int piece = D == 128 ? l8 : ct & 3;
                 uint4 w = *reinterpret_cast<const uint4*>(src + row * D + piece * 16);
-                if (clear && row >= lim) w = make_uint4(0, 0, 0, 0);
+                if (clear && (row < lead || row >= lim)) w = make_uint4(0, 0, 0, 0);
                 uint8_t* panel = dst + (piece >> 2) * S::kPanel;
                 const uint32_t c = (piece & 3) * 2;
                 *reinterpret_cast<uint4*>(panel + tc::sw128_offset(row, c)) =
@@ -596,17 +602,17 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv8_prefill(const __grid_consta
             bool ok = wait_warp(kLFull, st);
             if (tile >= 2) ok = ok && wait_warp(kKEmpty + st, ((tile >> 1) - 1) & 1);
             if (!ok) break;
-            const int lim = lims[tile & 7];
-            convert(smem + S::codes, smem + S::k + st * S::kTile, false, 0);
+            const int lim = lims[tile & 7] & 255, lead = lims[tile & 7] >> 8;
+            convert(smem + S::codes, smem + S::k + st * S::kTile, false, 0, 0);
             tc::fence_proxy_async_smem();
             tc::mbar_arrive(bars + kLEmpty);
             tc::mbar_arrive(bars + kKFull + st);
             ok = wait_warp(kLFull + 1, st);
             if (tile >= 2) ok = ok && wait_warp(kVEmpty + st, ((tile >> 1) - 1) & 1);
             if (!ok) break;
-            // values behind the sequence's end are zeros, whatever is there: a weight of 0 times NaN is NaN
-            if (lim < kPos) convert(smem + S::codes + kPos * D, smem + S::v + st * S::kTile, true, lim);
-            else convert(smem + S::codes + kPos * D, smem + S::v + st * S::kTile, false, 0);
+            // values behind the sequence's end, and where nothing was copied, are zeros: a weight of 0 times NaN is NaN
+            if (lim < kPos || lead) convert(smem + S::codes + kPos * D, smem + S::v + st * S::kTile, true, lead, lim);
+            else convert(smem + S::codes + kPos * D, smem + S::v + st * S::kTile, false, 0, 0);
             tc::fence_proxy_async_smem();
             tc::mbar_arrive(bars + kLEmpty + 1);
             tc::mbar_arrive(bars + kVFull + st);
@@ -617,19 +623,22 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv8_prefill(const __grid_consta
             // ------------------------------------------------------------ pages, scales and the codes' loads
             const int box = p.c.bs() < kPos ? p.c.bs() : kPos, boxes = kPos / box;
             uint32_t issued = 0, steps = (uint32_t)(u1 - u0);
-            int phys = -1, lim = 0, h = 0, e0 = 0;
+            int phys = -1, lim = 0, h = 0, e0 = 0;  // lim: positions before the sequence's end, and (<< 8) how many are not looked up
             bool fresh = true, item_ends = true;    // the tile is the first of its item in this piece
             auto look = [&](bool there) {    // lane x < 8: the block of positions 16 x .. of the tile at `cur`
                 phys = -1;
                 fresh = item_ends;
                 if (!there) return;
                 const int t0 = cur.lo + cur.step * kPos;
-                lim = cur.L - t0;
+                lim = cur.L - t0 < kPos ? (cur.L > t0 ? cur.L - t0 : 0) : kPos;
                 h = cur.h;
-                if (lane < 8 && lane * 16 < lim) {
+                const bool there_too = lane < 8 && line.seen(cur, t0 + lane * 16);
+                if (there_too) {
                     phys = kv8_block(p.c, cur.b, (t0 + lane * 16) >> p.c.bs_log2);
                     if (phys < 0) flag(p.a.status, kStatusBounds);
                 }
+                const uint32_t some = __ballot_sync(0xFFFFFFFFu, there_too);
+                lim |= (some ? __ffs(some) - 1 : 0) << 12;      // 16 of them a block
                 item_ends = ++cur.step >= cur.steps;
                 if (item_ends) line.next_item(cur);
             };

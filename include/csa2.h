@@ -605,7 +605,8 @@ CSA2_API csa2_status csa2_kv8_read(const csa2_kv8_cache* cache, const int32_t* s
  * lse = -inf.  The products take q and the codes as they are and accumulate in
  * fp32; the weights exp(z - max) are rounded to fp16 for the second product,
  * sums and lse use them unrounded.  What a block holds behind the sequence's
- * end does not enter, whatever it is.
+ * end does not enter, whatever it is; a block before the windows of all rows is
+ * not looked up, so its table entry may be anything.
  */
 CSA2_API csa2_status csa2_kv8_attn(const csa2_kv8_cache* cache, const void* q, csa2_dtype q_dtype, int64_t stride_b,
                                    int64_t stride_t, int T, int H, const int32_t* n_q, int window, float sm_scale,

@@ -523,6 +523,59 @@ def test_attn_many_rows_with_room_wait_that_runs_out(with_room):
     test_attn_many_rows_wait_that_runs_out()
 
 
+@pytest.mark.parametrize("room", [False, True])
+@pytest.mark.parametrize("bs,lens,T,G,window", [
+    (16, [500, 90], 1, 4, 20), (16, [500, 333], 3, 4, 77), (64, [700], 2, 8, 65), (16, [900, 613], 60, 8, 70),
+    (32, [900, 400, 385], 130, 16, 129), (64, [1000, 700], 200, 8, 300), (128, [1000, 999], 260, 8, 200)])
+def test_attn_window_with_the_pages_before_it_gone(request, bs, lens, T, G, window, room):
+    if room:
+        request.getfixturevalue("with_room")
+    dev, r = both_caches(len(lens), 2, 128, bs, (max(lens) + bs - 1) // bs)
+    fill(dev, r, lens)
+    q, out, lse = attend(dev, r, lens, T, 2 * G, window=window)
+    for b, L in enumerate(lens):
+        gone = max(0, L - T - window + 1) // bs          # blocks that no row sees
+        dev.block_table[b, :gone] = -1
+        assert gone
+    out2, lse2, ws = torch.zeros_like(out), torch.zeros_like(lse), workspace(dev, T, 2 * G)
+    csa2.kv8_attn(dev, q, out2, ws, lse=lse2, window=window)
+    assert csa2.read_device_status(ws) == csa2.OK
+    assert torch.allclose(out2.float(), out.float(), atol=2.0 ** -7, rtol=2.0 ** -7)
+    check_attn(dev, r, q, out2, lse2, [T] * len(lens), 1 / math.sqrt(128),
+               lambda b, j, h, p: np.arange(max(0, p - window + 1), p + 1), lens)
+
+
+def test_attn_many_rows_nonfinite_bad_pages_and_lengths(with_room):
+    lens, T = [500], 40
+    dev, r = both_caches(1, 2, 128, 64, 8)
+    fill(dev, r, lens)
+    q, out, lse = attend(dev, r, lens, T, 16)
+    again, ws = torch.zeros_like(out), workspace(dev, T, 16)
+    for _ in range(10):
+        csa2.kv8_attn(dev, q, again, ws)
+        assert torch.equal(again, out)
+    q2 = q.clone()
+    q2[0, 7, 3, 5], q2[0, 30, 6, 1] = math.nan, math.inf
+    out2, lse2 = torch.zeros_like(out), torch.zeros_like(lse)
+    csa2.kv8_attn(dev, q2, out2, ws, lse=lse2)
+    assert csa2.read_device_status(ws) == csa2.OK
+    keep = torch.ones(1, T, 16, dtype=torch.bool, device="cuda")
+    keep[0, 7, 3] = keep[0, 30, 6] = False
+    assert bool(out2[~keep].isnan().any(-1).all())
+    assert bool(out2[keep].isfinite().all())
+    assert torch.allclose(out2[keep].float(), out[keep].float(), atol=2.0 ** -7, rtol=2.0 ** -7)
+    table = dev.block_table.clone()
+    for bad in (-1, 1 << 20):
+        dev.block_table[0, 3] = bad
+        csa2.kv8_attn(dev, q, out2, ws)
+        assert csa2.read_device_status(ws) == csa2.ERR_DEVICE_BOUNDS
+    dev.block_table.copy_(table)
+    for n_q, L in (([T + 1], 500), ([-1], 500), (None, -1), (None, (1 << 20) + 1)):
+        dev.seq_lens.fill_(L)
+        csa2.kv8_attn(dev, q, out2, ws, n_q=None if n_q is None else i32(n_q))
+        assert csa2.read_device_status(ws) == csa2.ERR_DEVICE_BOUNDS
+
+
 @pytest.mark.parametrize("T", [1, 16, 24])
 @pytest.mark.parametrize("q_scale", [0.0, 2.0 ** -40, 2.0 ** -15])
 def test_attn_zero_keys_and_small_queries(with_room, T, q_scale):
