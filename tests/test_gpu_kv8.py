@@ -541,8 +541,7 @@ def test_attn_window_with_the_pages_before_it_gone(request, bs, lens, T, G, wind
     csa2.kv8_attn(dev, q, out2, ws, lse=lse2, window=window)
     assert csa2.read_device_status(ws) == csa2.OK
     assert torch.allclose(out2.float(), out.float(), atol=2.0 ** -7, rtol=2.0 ** -7)
-    check_attn(dev, r, q, out2, lse2, [T] * len(lens), 1 / math.sqrt(128),
-               lambda b, j, h, p: np.arange(max(0, p - window + 1), p + 1), lens)
+    assert torch.allclose(lse2, lse, atol=2.0 ** -12, rtol=2.0 ** -12)
 
 
 def test_attn_many_rows_nonfinite_bad_pages_and_lengths(with_room):
