@@ -138,20 +138,21 @@ struct Kv8Attn {
 bool kv8_row_map(CUtensorMap_st* map, const DevKv8& c, void* codes, int box_rows, bool swizzled);
 
 // The dense attention runs as the streaming kernel (kv8_attn.cu) for up to 16
-// query rows of a key head (tokens x query heads), and for more while its steps,
-// 16 rows by 128 positions as far as the cache reaches (the lengths are on the
-// device), are few; beyond that as the tensor-core kernel (kv8_prefill.cu), which
-// takes 256 rows a step but 10 us more to start.  Measured, streaming against
-// tensor cores: 1,024 steps (64 rows, 8 sequences of 512) 22.0 against 34.4 us,
-// 2,048 (128 rows of the same) 36.0 and 39.0, 4,096 (256 rows) 56.0 and 48.1; of 24
-// rows 4,096 steps (32 sequences of 1,024) 49.0 and 64.0, 16,384 about equal.
+// query rows of a key head (tokens x query heads), and for more while its cost is
+// small: steps of 16 rows by 128 positions as far as the cache reaches (the lengths
+// are on the device), and two an item for its queries and outputs.  Beyond that
+// the tensor-core kernel (kv8_prefill.cu) runs, which takes 256 rows a step but
+// 10 us more to start.  Measured, streaming against tensor cores: cost 1,536 (64
+// rows, 8 sequences of 512) 22.0 and 34.4 us, 2,160 (160 rows, 9 of 82) 24.7 and
+// 25.9, 4,536 (328 rows of the same) 42.3 and 28.5; of 24 rows 2,304 (8 sequences of
+// 2,048) 29.6 and 41.9, 5,120 (32 of 1,024) 49.0 and 64.0, 16,384 about equal.
 constexpr int64_t kKv8StreamRows = 16;
 inline bool kv8_streams(const DevKv8& c, const Kv8Attn& a) {
     const int64_t rows = (int64_t)a.q.T * (a.q.H / c.heads);
+    if (a.block_idx || rows <= kKv8StreamRows) return true;
     int64_t span = (int64_t)c.max_blocks << c.bs_log2;
     if (a.window && (int64_t)a.window + a.q.T < span) span = (int64_t)a.window + a.q.T;
-    return a.block_idx || rows <= kKv8StreamRows ||
-           (rows + 15) / 16 * c.batch * c.heads * ((span + 127) / 128) <= (rows <= 32 ? 4096 : 2048);
+    return (rows + 15) / 16 * c.batch * c.heads * ((span + 127) / 128 + 2) <= (rows <= 32 ? 5120 : 2560);
 }
 size_t kv8_attn_part_floats(int dim);
 size_t kv8_prefill_part_floats(int dim);

@@ -28,8 +28,12 @@
 // of two).
 //
 // Work split as in kv8_attn.cu: the (row block, head, 128 positions) steps of
-// the batch form one line cut into equal pieces, cut items are merged by
-// k_kv8_prefill_combine.
+// the batch, and kItem units an item, form one line cut into equal pieces; cut
+// items are merged by k_kv8_prefill_combine.  2,048 tokens over 8,192 positions
+// (32 / 8 heads of 128): 275 us = 0.87 PFLOP/s, 52 % of the measured bf16 rate.  A
+// step of a row tile is a chain of about 4,100 cycles (S to registers 250, weights
+// 1,500, the halves' agreement and the store 500, both products 1,100, looks at
+// barriers the rest), of which the other tile's covers a half.
 #include <cuda.h>
 #include <cuda_fp16.h>
 
@@ -61,6 +65,13 @@ struct Part {   // of a cut item: outputs [256][D], per row (m, l, M), then what
     static constexpr int kStats = kRows * D, kDesc = kStats + kRows * 3, kFloats = kDesc + 32;
 };
 
+// Units of the line that an item costs besides its steps: queries, the first
+// products and the outputs, with nothing else under way.  Without them the piece
+// with the most short items was the last by far: a prompt of 2,000 tokens, 32 / 8
+// heads, took 279 us, with 3 units 115, with 6 or 10 95; 2,048 tokens over 8,192
+// positions 278, 277, 275 and 272.
+constexpr int kItem = 8;
+
 // One step of the line: sequence b, row block rb, head h, positions lo + 128 *
 // step ...; rows: row0 .. row0 + rows - 1 of the sequence's (token, group) rows.
 struct Cursor {
@@ -89,7 +100,7 @@ struct Line {
         const int64_t seen = p1 + 1 - k.lo;
         k.steps = seen > 0 ? (int)((seen + kPos - 1) / kPos) : 1;  // an empty row still has to be written
     }
-    __device__ __forceinline__ int64_t total(const Cursor& k) const { return (int64_t)p.c.heads * k.steps; }
+    __device__ __forceinline__ int64_t total(const Cursor& k) const { return (int64_t)p.c.heads * (k.steps ? k.steps + kItem : 0); }
     // Whether position t's block is to be looked up: it holds positions, and not only
     // such as lie before every row's window (their page may be gone).
     __device__ __forceinline__ bool seen(const Cursor& k, int t) const {
@@ -135,7 +146,8 @@ __device__ int64_t line_sums(const Line& w, int64_t* sums, uint32_t* status) {
     return sums[kThreads];
 }
 
-__device__ void line_find(const Line& w, const int64_t* sums, int64_t u, Cursor& k) {
+// The item and step of unit u, and the units before its first step that are left.
+__device__ int line_find(const Line& w, const int64_t* sums, int64_t u, Cursor& k) {
     const int pairs = w.p.c.batch * w.p.row_blocks, per = (pairs + kThreads - 1) / kThreads;
     int lo = 0, hi = kThreads;
     while (hi - lo > 1) {
@@ -150,8 +162,38 @@ __device__ void line_find(const Line& w, const int64_t* sums, int64_t u, Cursor&
         if (u < t || pair + 1 >= pairs) break;
         u -= t;
     }
-    k.h = k.steps ? (int)(u / k.steps) : 0;
-    k.step = k.steps ? (int)(u - (int64_t)k.h * k.steps) : 0;
+    if (k.steps == 0) return 0;
+    k.h = (int)(u / (k.steps + kItem));
+    const int at = (int)(u - (int64_t)k.h * (k.steps + kItem));
+    k.step = at > kItem ? at - kItem : 0;
+    return at < kItem ? kItem - at : 0;
+}
+
+// Steps among `units` units from cursor k on, `ahead` of them before its first step.
+__device__ int line_steps(const Line& w, Cursor k, int64_t units, int ahead) {
+    const int pairs = w.p.c.batch * w.p.row_blocks;
+    int64_t n = 0;
+    while (units > ahead) {
+        units -= ahead;
+        const int64_t here = units < k.steps - k.step ? units : k.steps - k.step;
+        n += here;
+        units -= here;
+        if (units == 0) break;
+        // the other heads have the same steps
+        const int64_t each = k.steps + kItem, rest = w.p.c.heads - 1 - k.h, whole = units / each < rest ? units / each : rest;
+        n += whole * k.steps;
+        units -= whole * each;
+        if (whole < rest) {
+            if (units > kItem) n += units - kItem;
+            break;
+        }
+        int pair = k.pair;
+        do w.load(k, ++pair, nullptr);
+        while (pair < pairs && k.steps == 0);
+        if (pair >= pairs) break;
+        ahead = kItem;
+    }
+    return (int)n;
 }
 
 __device__ __forceinline__ float max3(float a, float b, float c) {
@@ -273,7 +315,11 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv8_prefill(const __grid_consta
     const bool any = blockIdx.x < share && total > 0;
     const int64_t u0 = any ? total * blockIdx.x / share : 0, u1 = any ? total * (blockIdx.x + 1) / share : 0;
     Cursor cur;
-    if (any) line_find(line, sums, u0, cur);
+    int piece_steps = 0;
+    if (any) {
+        const int ahead = line_find(line, sums, u0, cur);
+        piece_steps = line_steps(line, cur, u1 - u0, ahead);
+    }
     tc::fence_before_sync();
     __syncthreads();   // TMEM is there, the barriers are, and `sums` becomes the codes' place
     tc::fence_after_sync();
@@ -304,7 +350,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv8_prefill(const __grid_consta
         uint32_t tile = 0, s_phase = 0, o_phase = 0;   // tiles done by the CTA; parities
         bool ok = true;
         // Between items only this much of the cursor is kept (registers): the rest is worked out again.
-        int pair = cur.pair, head = cur.h, step = cur.step, todo_all = (int)(u1 - u0);
+        int pair = cur.pair, head = cur.h, step = cur.step, todo_all = piece_steps;
         auto item = [&]() {
             asm volatile("" : "+r"(pair));   // not to be kept from the time before
             Cursor k;
@@ -604,7 +650,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv8_prefill(const __grid_consta
                     make_uint4(half2_lo(w.z), half2_hi(w.z), half2_lo(w.w), half2_hi(w.w));
             }
         };
-        const int steps = (int)(u1 - u0);
+        const int steps = piece_steps;
         for (int tile = 0; tile < steps; ++tile) {
             const uint32_t st = tile & 1;
             bool ok = wait_warp(kLFull, st);
@@ -630,7 +676,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv8_prefill(const __grid_consta
         if (warp == kLoadWarp) {
             // ------------------------------------------------------------ pages, scales and the codes' loads
             const int box = p.c.bs() < kPos ? p.c.bs() : kPos, boxes = kPos / box;
-            uint32_t issued = 0, steps = (uint32_t)(u1 - u0);
+            uint32_t issued = 0, steps = (uint32_t)piece_steps;
             int phys = -1, lim = 0, h = 0, e0 = 0;  // lim: positions before the sequence's end, and (<< 8) how many are not looked up
             bool fresh = true, item_ends = true;    // the tile is the first of its item in this piece
             auto look = [&](bool there) {    // lane x < 8: the block of positions 16 x .. of the tile at `cur`
@@ -728,7 +774,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv8_prefill(const __grid_consta
                                        idesc_o, more || x + y > 0);
                 }
             };
-            int pair = cur.pair, head = cur.h, step = cur.step, todo_all = (int)(u1 - u0);
+            int pair = cur.pair, head = cur.h, step = cur.step, todo_all = piece_steps;
             while (todo_all > 0 && ok) {
                 int todo, tiles;
                 {
