@@ -384,36 +384,48 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv8_prefill(const __grid_consta
                 pos -= cur.lo + cur.step * kPos + half * 64;
                 first -= cur.lo + cur.step * kPos + half * 64;
                 if (!mine) pos = 0x7FFFFFFF, first = -0x7FFFFFFF;   // rows without a token: anything, without the mask
-                const uint16_t* src = static_cast<const uint16_t*>(p.a.q.q) + (int64_t)cur.b * p.a.q.stride_b +
-                                      (int64_t)j * p.a.q.stride_t + (int64_t)(cur.h * G + g) * D + half * (D / 2);
+                // a warp's 32 half rows by whole lines: kVec lanes a row, 32 / kVec rows at a time
+                const int64_t from = (int64_t)cur.b * p.a.q.stride_b + (int64_t)j * p.a.q.stride_t + (int64_t)(cur.h * G + g) * D;
+                const uint32_t live = __ballot_sync(0xFFFFFFFFu, mine);
+                const int piece = lane % kVec;
                 uint4 x[kVec];
 #pragma unroll
                 for (int i = 0; i < kVec; ++i) {
+                    const int at = i * (32 / kVec) + lane / kVec;
+                    const int64_t src = __shfl_sync(0xFFFFFFFFu, from, at);
                     x[i] = make_uint4(0, 0, 0, 0);
-                    if (mine) x[i] = __ldg(reinterpret_cast<const uint4*>(src) + i);
+                    if (live >> at & 1)
+                        x[i] = __ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.a.q.q) + src + half * (D / 2)) + piece);
                 }
                 if (p.a.q.is_bf16) {
-                    float amax = 0.0f;
+                    float amax[kVec];
 #pragma unroll
                     for (int i = 0; i < kVec; ++i) {
                         const uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+                        amax[i] = 0.0f;
 #pragma unroll
                         for (int q = 0; q < 4; ++q) {
                             const float a = fabsf(__uint_as_float(w[q] << 16)), b = fabsf(__uint_as_float(w[q] & 0xFFFF0000u));
-                            if (a <= 3.4028235e38f) amax = fmaxf(amax, a);
-                            if (b <= 3.4028235e38f) amax = fmaxf(amax, b);
+                            if (a <= 3.4028235e38f) amax[i] = fmaxf(amax[i], a);
+                            if (b <= 3.4028235e38f) amax[i] = fmaxf(amax[i], b);
                         }
+#pragma unroll
+                        for (int o = 1; o < kVec; o <<= 1) amax[i] = fmaxf(amax[i], __shfl_xor_sync(0xFFFFFFFFu, amax[i], o));
                     }
                     ok = agree(ok);              // the sums of the item before have been read
-                    xch[half * 128 + rt] = amax;
+                    const int r0 = (warp & 3) * 32;
+#pragma unroll
+                    for (int i = 0; i < kVec; ++i)
+                        if (piece == 0) xch[half * 128 + r0 + i * (32 / kVec) + lane / kVec] = amax[i];
                     ok = agree(ok);
-                    amax = fmaxf(amax, xch[(half ^ 1) * 128 + rt]);
-                    int e = 14 - ((int)(__float_as_uint(amax) >> 23) - 127);
-                    e = e > 126 ? 126 : e;
-                    const float up = exp2_int(e);
-                    zs *= exp2_int(-e);
+                    auto up_of = [&](float m) {
+                        const int e = 14 - ((int)(__float_as_uint(m) >> 23) - 127);
+                        return e > 126 ? 126 : e;
+                    };
+                    zs *= exp2_int(-up_of(fmaxf(xch[rt], xch[128 + rt])));
 #pragma unroll
                     for (int i = 0; i < kVec; ++i) {
+                        const float up = exp2_int(up_of(fmaxf(amax[i], xch[(half ^ 1) * 128 + r0 + i * (32 / kVec) + lane / kVec])));
                         uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
 #pragma unroll
                         for (int q = 0; q < 4; ++q) {
@@ -425,11 +437,11 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv8_prefill(const __grid_consta
                     }
                 }
                 uint8_t* dst = smem + S::q + t * S::kTile;
+                const int c = half * kVec + piece;
 #pragma unroll
-                for (int i = 0; i < kVec; ++i) {
-                    const int c = half * kVec + i;
-                    *reinterpret_cast<uint4*>(dst + (c >> 3) * S::kPanel + tc::sw128_offset(rt, c & 7)) = x[i];
-                }
+                for (int i = 0; i < kVec; ++i)
+                    *reinterpret_cast<uint4*>(dst + (c >> 3) * S::kPanel +
+                                              tc::sw128_offset((warp & 3) * 32 + i * (32 / kVec) + lane / kVec, c & 7)) = x[i];
                 tc::fence_proxy_async_smem();
                 tc::mbar_arrive(bars + kQ);
             }
@@ -558,12 +570,12 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv8_prefill(const __grid_consta
             const float f = l == 0.0f ? 0.0f : exp2_int((int)e0) / l;
             if (ok && (!dual || t == 0)) {
                 const float* odd = reinterpret_cast<const float*>(smem + S::q);
+                const uint32_t live = __ballot_sync(0xFFFFFFFFu, mine);
 #pragma unroll 1
                 for (int q = 0; q < D / 2; q += 32) {
                     uint32_t r[32];
                     tc::tmem_ld32_nowait(col_o + q, r);
                     tc::tmem_ld_wait();
-                    if (!mine) continue;
                     const int ch = half * (D / 2) + q;
                     if (dual) {
 #pragma unroll
@@ -571,7 +583,15 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv8_prefill(const __grid_consta
                             r[x] = __float_as_uint(__uint_as_float(r[x]) * f0 + odd[(ch + x) * 128 + rt] * f1);
                     }
                     if (whole) {
-                        uint4* dst = reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.a.out) + at * D + ch);
+                        // through shared memory, two rows of 64 bytes in 128, so that they leave by lines: over the
+                        // queries, or over what this warp alone has read of the odd steps' output
+                        __syncwarp();
+                        auto stage = [&](int row, int chunk) {
+                            const int pair = row >> 1;
+                            uint8_t* at = dual ? smem + S::q + ((ch + pair) * 128 + (warp & 3) * 32) * 4
+                                               : smem + S::q + t * S::kTile + (warp & 7) * 2048 + pair * 128;
+                            return reinterpret_cast<uint4*>(at + (row & 1) * 64 + ((chunk ^ (pair & 3)) << 4));
+                        };
 #pragma unroll
                         for (int x = 0; x < 4; ++x) {
                             uint32_t w[4];
@@ -586,9 +606,18 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv8_prefill(const __grid_consta
                                     memcpy(&w[y], &h, 4);
                                 }
                             }
-                            dst[x] = make_uint4(w[0], w[1], w[2], w[3]);
+                            *stage(lane, x) = make_uint4(w[0], w[1], w[2], w[3]);
                         }
-                    } else {
+                        __syncwarp();
+#pragma unroll
+                        for (int x = 0; x < 4; ++x) {
+                            const int from = x * 8 + (lane >> 2);
+                            const int64_t to = __shfl_sync(0xFFFFFFFFu, at, from);
+                            if (live >> from & 1)
+                                *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.a.out) + to * D + ch + (lane & 3) * 8) =
+                                    *stage(from, lane & 3);
+                        }
+                    } else if (mine) {
                         // by 16-byte columns across the rows, so that a warp's stores are dense
                         float4* dst = reinterpret_cast<float4*>(part) + (int64_t)(ch / 4) * kRows + row;
 #pragma unroll
