@@ -30,7 +30,7 @@
 // Work split as in kv8_attn.cu: the (row block, head, 128 positions) steps of
 // the batch, and kItem units an item, form one line cut into equal pieces; cut
 // items are merged by k_kv8_prefill_combine.  2,048 tokens over 8,192 positions
-// (32 / 8 heads of 128): 275 us = 0.87 PFLOP/s, 52 % of the measured bf16 rate.  A
+// (32 / 8 heads of 128): 270 us = 0.89 PFLOP/s, 53 % of the measured bf16 rate.  A
 // step of a row tile is a chain of about 4,100 cycles (S to registers 250, weights
 // 1,500, the halves' agreement and the store 500, both products 1,100, looks at
 // barriers the rest), of which the other tile's covers a half.
@@ -68,8 +68,8 @@ struct Part {   // of a cut item: outputs [256][D], per row (m, l, M), then what
 // Units of the line that an item costs besides its steps: queries, the first
 // products and the outputs, with nothing else under way.  Without them the piece
 // with the most short items was the last by far: a prompt of 2,000 tokens, 32 / 8
-// heads, took 279 us, with 3 units 115, with 6 or 10 95; 2,048 tokens over 8,192
-// positions 278, 277, 275 and 272.
+// heads, took 279 us, with 3 units 115, with 6 or 10 95 (8 and rows by whole lines:
+// 92); 2,048 tokens over 8,192 positions 278, 277, 275 and 272.
 constexpr int kItem = 8;
 
 // One step of the line: sequence b, row block rb, head h, positions lo + 128 *
