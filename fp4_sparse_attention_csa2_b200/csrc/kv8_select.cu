@@ -304,24 +304,26 @@ __global__ void __launch_bounds__(kThreads, kPerSm) k_kv8_score(const __grid_con
 }
 
 // ---------------------------------------------------------------- the best blocks of a row
-constexpr int kSelThreads = 1024;
-constexpr int kBins = 2048;
 constexpr int kCand = 2048;      // candidates resolved by rank
 
+template <int THREADS>
 struct SelSmem {
+    static constexpr int kBins = 2 * THREADS, kWarps = THREADS / 32;
     uint32_t hist[kBins];
     uint32_t cand_key[kCand];
     int cand_idx[kCand];
-    uint32_t red[32][2];
+    uint32_t red[kWarps][2];
     int n_cand, bin, above;
 };
 
-__device__ __forceinline__ uint32_t block_sum(uint32_t v, SelSmem& s) {
+template <int THREADS>
+__device__ __forceinline__ uint32_t block_sum(uint32_t v, SelSmem<THREADS>& s) {
     v = __reduce_add_sync(0xFFFFFFFFu, v);
     __syncthreads();
     if ((threadIdx.x & 31) == 0) s.red[threadIdx.x >> 5][0] = v;
     __syncthreads();
-    return __reduce_add_sync(0xFFFFFFFFu, s.red[threadIdx.x & 31][0]);
+    const int lane = threadIdx.x & 31;
+    return __reduce_add_sync(0xFFFFFFFFu, lane < THREADS / 32 ? s.red[lane][0] : 0u);
 }
 
 // One CTA per row.  The blocks that compete are those between the first and
@@ -332,9 +334,10 @@ __device__ __forceinline__ uint32_t block_sum(uint32_t v, SelSmem& s) {
 // The chosen are bits of a map over the row's blocks, read out in order.  KPT
 // keys a thread stay in registers, fetched before the row's length is known;
 // KPT == 0: rows of any length, keys kept in the scores' place.
-template <int KPT>
-__global__ void __launch_bounds__(kSelThreads) k_kv8_select(const __grid_constant__ Params p) {
-    __shared__ SelSmem s;
+template <int KPT, int THREADS>
+__global__ void __launch_bounds__(THREADS) k_kv8_select(const __grid_constant__ Params p) {
+    constexpr int kBins = SelSmem<THREADS>::kBins, kSelWarps = THREADS / 32;
+    __shared__ SelSmem<THREADS> s;
     extern __shared__ uint32_t map[];                          // a bit a block
     pdl_begin();
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -344,7 +347,7 @@ __global__ void __launch_bounds__(kSelThreads) k_kv8_select(const __grid_constan
     if (KPT) {
 #pragma unroll
         for (int i = 0; i < kKeys; ++i) {
-            const int at = i * kSelThreads + tid;
+            const int at = i * THREADS + tid;
             reg[i] = at < p.c.max_blocks ? row[at] : 0u;
         }
     }
@@ -353,7 +356,7 @@ __global__ void __launch_bounds__(kSelThreads) k_kv8_select(const __grid_constan
     if (!row_of(p, b, bj - b * p.q.T, visible, false)) return;
     int32_t* out = p.idx + (int64_t)blockIdx.x * p.n_sel;
     if (visible <= p.n_sel) {
-        for (int i = tid; i < p.n_sel; i += kSelThreads) out[i] = i < visible ? i : -1;
+        for (int i = tid; i < p.n_sel; i += THREADS) out[i] = i < visible ? i : -1;
         return;
     }
     const int c0 = p.n_first, c1 = visible - p.n_recent;       // competing blocks [c0, c1); c0 <= c1 as n_sel < visible
@@ -367,12 +370,12 @@ __global__ void __launch_bounds__(kSelThreads) k_kv8_select(const __grid_constan
         if (KPT) {
 #pragma unroll
             for (int i = 0; i < kKeys; ++i) {
-                const int at = i * kSelThreads + tid;
+                const int at = i * THREADS + tid;
                 if (at >= c0 && at < c1) f(at, reg[i]);
             }
         } else {
 #pragma unroll 4
-            for (int at = c0 + tid; at < c1; at += kSelThreads) f(at, row[at]);
+            for (int at = c0 + tid; at < c1; at += THREADS) f(at, row[at]);
         }
     };
     auto choose = [&](int at) { atomicOr(map + (at >> 5), 1u << (at & 31)); };
@@ -381,7 +384,7 @@ __global__ void __launch_bounds__(kSelThreads) k_kv8_select(const __grid_constan
 #pragma unroll
         for (int i = 0; i < kKeys; ++i) reg[i] = key_of(reg[i]);
     } else {
-        for (int at = c0 + tid; at < c1; at += kSelThreads) row[at] = key_of(row[at]);
+        for (int at = c0 + tid; at < c1; at += THREADS) row[at] = key_of(row[at]);
     }
     each([&](int, uint32_t key) {
         lo = min(lo, key);
@@ -390,8 +393,8 @@ __global__ void __launch_bounds__(kSelThreads) k_kv8_select(const __grid_constan
     lo = __reduce_min_sync(0xFFFFFFFFu, lo);
     hi = __reduce_max_sync(0xFFFFFFFFu, hi);
     if (lane == 0) s.red[warp][0] = lo, s.red[warp][1] = hi;
-    for (int i = tid; i < kBins; i += kSelThreads) s.hist[i] = 0;
-    for (int i = tid; i < words; i += kSelThreads) {           // the first and the newest are chosen
+    for (int i = tid; i < kBins; i += THREADS) s.hist[i] = 0;
+    for (int i = tid; i < words; i += THREADS) {           // the first and the newest are chosen
         uint32_t m = 0;
         for (int x = i * 32; x < i * 32 + 32; ++x)
             if (x < c0 || (x >= c1 && x < visible)) m |= 1u << (x & 31);
@@ -399,8 +402,8 @@ __global__ void __launch_bounds__(kSelThreads) k_kv8_select(const __grid_constan
     }
     if (tid == 0) s.n_cand = 0;
     __syncthreads();
-    lo = __reduce_min_sync(0xFFFFFFFFu, s.red[lane][0]);       // 32 warps
-    hi = __reduce_max_sync(0xFFFFFFFFu, s.red[lane][1]);
+    lo = __reduce_min_sync(0xFFFFFFFFu, lane < kSelWarps ? s.red[lane][0] : 0xFFFFFFFFu);
+    hi = __reduce_max_sync(0xFFFFFFFFu, lane < kSelWarps ? s.red[lane][1] : 0u);
     const float flo = lo ? key_score(lo) : -INFINITY, fhi = hi ? key_score(hi) : -INFINITY;
     const float per = (float)(kBins - 1) / (fhi - flo);
     const bool linear = fhi - flo > 0.0f && fhi - flo < INFINITY && per < INFINITY;
@@ -422,8 +425,7 @@ __global__ void __launch_bounds__(kSelThreads) k_kv8_select(const __grid_constan
             }
             if (lane == 31) s.red[warp][0] = inc;
             __syncthreads();
-            uint32_t w = s.red[lane][0];
-            w = __reduce_add_sync(0xFFFFFFFFu, lane < warp ? w : 0u);
+            const uint32_t w = __reduce_add_sync(0xFFFFFFFFu, lane < warp ? s.red[lane][0] : 0u);
             const uint32_t after = w + inc, before = after - n;
             if (before < (uint32_t)want && after >= (uint32_t)want) {
                 const bool second = before + n0 < (uint32_t)want;
@@ -444,7 +446,7 @@ __global__ void __launch_bounds__(kSelThreads) k_kv8_select(const __grid_constan
                 }
             });
             __syncthreads();
-            for (int i = warp; i < members; i += 32) {          // a warp a member
+            for (int i = warp; i < members; i += kSelWarps) {          // a warp a member
                 const uint32_t key = s.cand_key[i];
                 const int at = s.cand_idx[i];
                 int rank = 0;
@@ -484,9 +486,9 @@ __global__ void __launch_bounds__(kSelThreads) k_kv8_select(const __grid_constan
         });
     }
     __syncthreads();
-    // ---- the map in order: kSelThreads words at a time
+    // ---- the map in order: THREADS words at a time
     int base = 0;
-    for (int i0 = 0; i0 < words; i0 += kSelThreads) {
+    for (int i0 = 0; i0 < words; i0 += THREADS) {
         uint32_t m = i0 + tid < words ? map[i0 + tid] : 0u;
         const uint32_t n = __popc(m);
         uint32_t inc = n;
@@ -497,14 +499,14 @@ __global__ void __launch_bounds__(kSelThreads) k_kv8_select(const __grid_constan
         }
         if (lane == 31) s.red[warp][1] = inc;
         __syncthreads();
-        const uint32_t w = s.red[lane][1];
+        const uint32_t w = lane < kSelWarps ? s.red[lane][1] : 0u;
         int at = base + (int)(__reduce_add_sync(0xFFFFFFFFu, lane < warp ? w : 0u) + inc - n);
         base += (int)__reduce_add_sync(0xFFFFFFFFu, w);
         for (; m; m &= m - 1) {
             if (at < p.n_sel) out[at] = (i0 + tid) * 32 + __ffs(m) - 1;
             ++at;
         }
-        if (i0 + kSelThreads < words) __syncthreads();
+        if (i0 + THREADS < words) __syncthreads();
     }
 }
 
@@ -533,14 +535,19 @@ cudaError_t launch_kv8_select(const DevKv8& c, const Kv8Query& q, int n_sel, int
     e = c.dim == 64 ? launch_pdl(k_kv8_score<64>, ctas, kThreads, ring, st, p)
                     : launch_pdl(k_kv8_score<128>, ctas, kThreads, ring, st, p);
     if (e != cudaSuccess) return e;
-    const auto select = c.max_blocks <= 2 * kSelThreads    ? k_kv8_select<2>
-                        : c.max_blocks <= 8 * kSelThreads  ? k_kv8_select<8>
-                        : c.max_blocks <= 17 * kSelThreads ? k_kv8_select<17>
-                                                           : k_kv8_select<0>;
+    // rows of up to 512 blocks by 256 threads each, so that more of them run at once: 4,096 rows
+    // of 256 blocks, with the scores, 104 us with 1,024 threads and 59 with 256, one row of 8 heads
+    // over 512 blocks 8.0 and 7.2 (512 rows of 768 blocks 36.4 and 37.7)
+    const bool small = c.max_blocks <= 512;
+    const auto select = small                       ? k_kv8_select<2, 256>
+                        : c.max_blocks <= 2 * 1024  ? k_kv8_select<2, 1024>
+                        : c.max_blocks <= 8 * 1024  ? k_kv8_select<8, 1024>
+                        : c.max_blocks <= 17 * 1024 ? k_kv8_select<17, 1024>
+                                                    : k_kv8_select<0, 1024>;
     const int map_bytes = (c.max_blocks + 31) / 32 * 4;
     if (map_bytes > 16 * 1024) e = cudaFuncSetAttribute(select, cudaFuncAttributeMaxDynamicSharedMemorySize, map_bytes);
     if (e != cudaSuccess) return e;
-    return launch_pdl(select, dim3(rows), kSelThreads, map_bytes, st, p);
+    return launch_pdl(select, dim3(rows), small ? 256 : 1024, map_bytes, st, p);
 }
 
 }  // namespace csa2

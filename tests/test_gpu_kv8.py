@@ -684,6 +684,13 @@ def test_select_among_many_blocks_and_equal_scores(bs, L, ties):
     check_select(r, q, idx, [L], [1], 2, 3)
 
 
+@pytest.mark.parametrize("bs,L", [(64, 30000), (16, 20000), (16, 200000)])
+@pytest.mark.parametrize("ties", [0, 1, 2])
+def test_select_among_fewer_blocks(bs, L, ties):
+    # rows of every width that the selection has a form for
+    test_select_among_many_blocks_and_equal_scores(bs, L, ties)
+
+
 def test_select_nonfinite_query_and_padding():
     lens, n = [300, 400], [2, 0]
     dev, r = both_caches(2, 1, 64, 16, 26)
