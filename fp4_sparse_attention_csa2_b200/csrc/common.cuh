@@ -11,7 +11,6 @@ namespace csa2 {
 // Sticky status bits ORed into the workspace status word by kernels.
 constexpr uint32_t kStatusBounds = 1u;
 constexpr uint32_t kStatusTimeout = 2u;
-constexpr uint32_t kStatusNonFinite = 4u;
 
 // A by-value copy of csa2_cache plus the derived per-sequence capacity.
 struct DevCache {

@@ -41,7 +41,7 @@
 
 #include "kernels.h"
 #include "kv8.cuh"
-#include "tc.cuh"
+#include "kv8_tc.cuh"
 
 namespace csa2 {
 namespace {

@@ -39,7 +39,7 @@
 
 #include "kernels.h"
 #include "kv8.cuh"
-#include "tc.cuh"
+#include "kv8_tc.cuh"
 
 namespace csa2 {
 namespace {
@@ -1047,7 +1047,8 @@ cudaError_t launch_kv8_prefill(const DevKv8& c, const Kv8Attn& a, cudaStream_t s
     p.a = a;
     p.G = a.q.H / c.heads;
     p.row_blocks = (int)(((int64_t)a.q.T * p.G + kRows - 1) / kRows);
-    p.wait_limit = wait_limit() * 16;      // looks of 4 us, not 65
+    const uint32_t tries = wait_limit();
+    p.wait_limit = tries < 1u << 28 ? tries * 16 : 0xFFFFFFFFu;   // looks of 4 us, not 65
     int dev = 0, sms = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
