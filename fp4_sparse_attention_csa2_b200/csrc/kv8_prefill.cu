@@ -24,8 +24,14 @@
 //   - one warp that looks up pages and issues the TMA loads.
 // Key scales multiply S per block; value scales enter the weights' exponent,
 // weight = 2^(z + log2(vs) - M), so the fp16 weights stay in range whatever the
-// blocks' scales are, and the sum takes them back out per block (exact powers
-// of two).
+// blocks' scales are.  The sum of 2^z does not depend on them, and takes them
+// back out per block (exact powers of two) where they lie within 2^kSpread of
+// the item's first block's: a weight that fp32 cannot hold is then nothing to
+// the sum either.  A tile with another scale (a block of zeros has the least,
+// 2^-120, but so have values of 1e-35), and every tile behind one with a far
+// greater scale, has its sum worked out from S for itself, without the value
+// scales (2,048 tokens over 8,192 positions with zeros for every other block's
+// values: 401 us, without 260).
 //
 // Work split as in kv8_attn.cu: the (row block, head, 128 positions) steps of
 // the batch, and kItem units an item, form one line cut into equal pieces; cut
@@ -52,6 +58,11 @@ constexpr int kMergeWarps = 16, kFewItems = 16;   // of a CTA of k_kv8_prefill_c
 constexpr float kNone = -3.0e38f;
 constexpr float kHeadroom = 8.0f;   // weights are 2^(z - M + 8): full fp16 precision down to 2^-22
 constexpr float kLazy = 7.0f;       // and at most 2^15 (fp16: 65504) before the maximum is moved
+// log2 of how far a block's value scale may be from the sums' unit 2^e0 for the
+// weights to carry the sum.  With scales within 2^48 of each other a weight that
+// underflows, 2^-126, is below 2^-86 of the greatest term of the sum.
+constexpr int kSpread = 24;
+constexpr float kApart = 64.0f;     // log2 of how far a sum's unit may be from another for it to be kept in that
 
 struct Params {
     DevKv8 c;
@@ -222,12 +233,53 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
     return r;
 }
 
-// log2 of the value scale that an item's sums are kept in, from its first
-// block's scale.
+// log2 of the value scale that an item's sums are kept in: its first block's.
+// The least scale is mostly that of a block of zeros and says nothing of the
+// others: 1 then, which is as right as any and nearer to most.
 __device__ __forceinline__ int sum_scale(float vs) {
     const int e = (int)(__float_as_uint(vs) >> 23) - 127;
-    return e == -120 ? 0 : (e < -100 ? -100 : (e > 100 ? 100 : e));
+    return e <= -120 ? 0 : (e > 120 ? 120 : e);
 }
+
+// A sum l of 2^z in units of 2^(M - 8 - e0 - x), x a whole number and mostly 0.
+struct Sum {
+    float l, x;
+    // l to [1, 2), where it is a number that has an exponent.
+    __device__ __forceinline__ void normalise() {
+        const int u = __float_as_int(l), e = u >> 23;
+        if (e > 0 && e < 255) {
+            l = __int_as_float((u & 0x7FFFFF) | 0x3F800000);
+            x -= (float)(e - 127);
+        }
+    }
+    // The maximum M rises by d.
+    __device__ __forceinline__ void rise(float d) {
+        if (d <= kApart || l == 0.0f) {
+            l *= ex2(-d);
+            if (l < 0x1p-40f) normalise();
+        } else {
+            const float k = rintf(d);
+            l *= ex2(k - d);
+            x += k;
+        }
+    }
+    // A sum with the same M.
+    __device__ __forceinline__ void add(Sum o) {
+        if (x == 0.0f && o.x == 0.0f) {
+            l += o.l;
+            return;
+        }
+        normalise();
+        o.normalise();
+        const float to = l == 0.0f ? o.x : o.l == 0.0f ? x : fminf(x, o.x);
+        l = l * ex2(fminf(to - x, 0.0f)) + o.l * ex2(fminf(to - o.x, 0.0f));
+        x = to;
+        if (fabsf(x) <= kApart) {
+            l *= ex2(-x);
+            x = 0.0f;
+        }
+    }
+};
 
 template <int D>
 struct Smem {
@@ -240,7 +292,7 @@ struct Smem {
     static constexpr int codes = v + 2 * kTile;               // K, V as stored
     static constexpr int sums = codes;                        // kThreads + 1 words, before the first load
     static constexpr int sc = codes + 2 * kPos * D;           // [8][8] key scale, log2 of the value scale
-    static constexpr int sg = sc + 8 * 8 * 8;                 // [8][8] 2^(e0 - that)
+    static constexpr int sg = sc + 8 * 8 * 8;                 // [8][8] 2^(e0 - that); 0: the weights do not carry the sum
     static constexpr int lims = sg + 8 * 8 * 4;               // [8] positions of a tile that are values
     static constexpr int xch = lims + 8 * 4;                  // [tile][half][128] floats: halves of a row agree
     static constexpr int bars = xch + 4 * 128 * 4;
@@ -362,7 +414,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv8_prefill(const __grid_consta
         while (todo_all > 0) {
             int todo, pos, first;
             bool dual;      // one row tile, even and odd steps apart
-            float e0;       // the value scale that sums are kept in: log2 of the item's first block's
+            float e0;       // log2 of the value scale that sums are kept in
             float zs = p.a.sm_scale * 1.4426950408889634f;
             {   // half a query row as fp16, K-major; bf16 scaled by the power of two that takes the row's
                 // greatest finite magnitude to [2^14, 2^15)
@@ -445,94 +497,204 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv8_prefill(const __grid_consta
                 tc::fence_proxy_async_smem();
                 tc::mbar_arrive(bars + kQ);
             }
-            float M = kNone, l = 0.0f;
+            float M = kNone;
+            Sum sum = {0.0f, 0.0f};
             bool started = false;      // O holds something
-            for (int i = 0; i < todo; ++i, ++tile) {
-                if (dual && (i & 1) != t) continue;
-                const int t0 = i * kPos;
-                ok = wait_warp(kS + t, s_phase) && ok;
-                s_phase ^= 1;
-                tc::fence_after_sync();
-                const float2* f2 = sc + (tile & 7) * 8 + half * 4;
-                const float* g1 = sg + (tile & 7) * 8 + half * 4;
-                const bool edge = !__all_sync(0xFFFFFFFFu, t0 + 63 <= pos && t0 >= first);
-                uint32_t w[32];        // weights, two a word
-                float l1;
+            bool wide = false;         // the sum is in a unit of its own
+            int i = 0;
+            while (i < todo) {
+                for (; !wide && i < todo; ++i, ++tile) {
+                    if (dual && (i & 1) != t) continue;
+                    const int t0 = i * kPos;
+                    ok = wait_warp(kS + t, s_phase) && ok;
+                    s_phase ^= 1;
+                    tc::fence_after_sync();
+                    const float2* f2 = sc + (tile & 7) * 8 + half * 4;
+                    const float* g1 = sg + (tile & 7) * 8 + half * 4;
+                    const bool edge = !__all_sync(0xFFFFFFFFu, t0 + 63 <= pos && t0 >= first);
+                    if (ok && g1[0] == 0.0f) break;        // goes on below (everyone where a wait ran out goes the same way)
+                    uint32_t w[32];        // weights, two a word
+                    float l1;
 #pragma unroll 1
-                for (;;) {
-                    uint32_t r[64];
-                    tc::tmem_ld32_nowait(col_s + half * 64, r);
-                    tc::tmem_ld32_nowait(col_s + half * 64 + 32, r + 32);
-                    tc::tmem_ld_wait();
-                    if (edge) {
+                    for (;;) {
+                        uint32_t r[64];
+                        tc::tmem_ld32_nowait(col_s + half * 64, r);
+                        tc::tmem_ld32_nowait(col_s + half * 64 + 32, r + 32);
+                        tc::tmem_ld_wait();
+                        if (edge) {
 #pragma unroll
-                        for (int x = 0; x < 64; ++x)
-                            if (t0 + x > pos || t0 + x < first) r[x] = 0xFF800000u;
+                            for (int x = 0; x < 64; ++x)
+                                if (t0 + x > pos || t0 + x < first) r[x] = 0xFF800000u;
+                        }
+                        float top = -INFINITY;     // the greatest logit + log2(value scale) of the half row
+                        l1 = 0.0f;
+#pragma unroll
+                        for (int q = 0; q < 4; ++q) {
+                            const uint32_t* v = r + q * 16;
+                            const float2 f = f2[q];
+                            // at least the least normal number: 0 times a masked -inf would be NaN, and what is
+                            // added to a logit, |S| < 2^31, is below 2^-95
+                            const float a = fmaxf(zs * f.x, 1.17549435e-38f), d = f.y - M + kHeadroom;
+                            const uint64_t ff = pack2(a, a), dd = pack2(d, d);
+                            uint64_t acc = 0;
+                            float m = __uint_as_float(v[0]);
+#pragma unroll
+                            for (int x = 0; x < 16; x += 2) {
+                                m = x ? max3(m, __uint_as_float(v[x]), __uint_as_float(v[x + 1])) : fmaxf(m, __uint_as_float(v[1]));
+                                const float2 z = unpack2(fma2(pack2(__uint_as_float(v[x]), __uint_as_float(v[x + 1])), ff, dd));
+                                const float2 e = make_float2(ex2(z.x), ex2(z.y));
+                                acc = add2(acc, pack2(e.x, e.y));
+                                const __half2 h = __floats2half2_rn(e.x, e.y);
+                                memcpy(&w[q * 8 + x / 2], &h, 4);
+                            }
+                            top = fmaxf(top, m * a + f.y);
+                            // back from 2^(z + log2 vs - M + 8) to 2^(z + e0 - M + 8), exactly
+                            const float2 s2 = unpack2(acc);
+                            l1 += (s2.x + s2.y) * g1[q];
+                        }
+                        // all of S is in registers from here: the weights may go over it
+                        if (agree(ok && !(top > M + kLazy))) break;
+                        xch[half * 128 + rt] = top;
+                        ok = agree(ok);
+                        if (!ok) break;
+                        const float M1 = fmaxf(M, fmaxf(top, xch[(half ^ 1) * 128 + rt])), f = ex2(M - M1);
+                        sum.l *= f;
+                        M = M1;
+                        if (started) {
+#pragma unroll 1
+                            for (int q = 0; q < D / 2; q += 16) {
+                                uint32_t o[16];
+                                tc::tmem_ld16_nowait(col_o + q, o);
+                                tc::tmem_ld_wait();
+#pragma unroll
+                                for (int x = 0; x < 16; ++x) o[x] = __float_as_uint(__uint_as_float(o[x]) * f);
+                                tc::tmem_st16_nowait(col_o + q, o);
+                            }
+                        }
+                        ok = agree(ok);            // the other half has read this one's maximum
+                        if (!ok) break;
                     }
-                    float top = -INFINITY;     // the greatest logit + log2(value scale) of the half row
-                    l1 = 0.0f;
+                    if (!ok) break;
+                    sum.l += l1;
+                    started = true;
+                    tc::tmem_st16_nowait(col_s + half * 32, w);
+                    tc::tmem_st16_nowait(col_s + half * 32 + 16, w + 16);
+                    tc::tmem_st_wait();
+                    tc::fence_before_sync();
+                    tc::mbar_arrive(bars + kP + t);
+                }
+                if (!ok || i >= todo) break;
+                // A step whose weights do not carry the sum, or the sum is in another unit: S is read for both maxima
+                // first, then for the weights and the sum's terms, whose greatest is near 1.
+                if (!(dual && (i & 1) != t)) {
+                    const int t0 = i * kPos;
+                    if (wide) {
+                        ok = wait_warp(kS + t, s_phase);
+                        s_phase ^= 1;
+                        tc::fence_after_sync();
+                    }
+                    const float2* f2 = sc + (tile & 7) * 8 + half * 4;
+                    const bool edge = !__all_sync(0xFFFFFFFFu, t0 + 63 <= pos && t0 >= first);
+                    auto logits = [&](int q, uint32_t* v) {        // 16 columns of S, and the factor to a logit
+                        tc::tmem_ld16_nowait(col_s + half * 64 + q * 16, v);
+                        tc::tmem_ld_wait();
+                        if (edge) {
 #pragma unroll
+                            for (int x = 0; x < 16; ++x)
+                                if (t0 + q * 16 + x > pos || t0 + q * 16 + x < first) v[x] = 0xFF800000u;
+                        }
+                        return fmaxf(zs * f2[q].x, 1.17549435e-38f);
+                    };
+                    float top = -INFINITY, most = -INFINITY;       // of logit + log2(value scale), and of the logits
+#pragma unroll 1
                     for (int q = 0; q < 4; ++q) {
-                        const uint32_t* v = r + q * 16;
-                        const float2 f = f2[q];
-                        // at least the least normal number: 0 times a masked -inf would be NaN, and what is
-                        // added to a logit, |S| < 2^31, is below 2^-95
-                        const float a = fmaxf(zs * f.x, 1.17549435e-38f), d = f.y - M + kHeadroom;
-                        const uint64_t ff = pack2(a, a), dd = pack2(d, d);
-                        uint64_t sum = 0;
+                        uint32_t v[16];
+                        const float a = logits(q, v);
                         float m = __uint_as_float(v[0]);
 #pragma unroll
+                        for (int x = 1; x < 15; x += 2) m = max3(m, __uint_as_float(v[x]), __uint_as_float(v[x + 1]));
+                        m = fmaxf(m, __uint_as_float(v[15]));
+                        top = fmaxf(top, m * a + f2[q].y);
+                        most = fmaxf(most, m * a);
+                    }
+                    if (!agree(ok && !(top > M + kLazy))) {
+                        xch[half * 128 + rt] = top;
+                        ok = agree(ok);
+                        if (!ok) break;
+                        const float M1 = fmaxf(M, fmaxf(top, xch[(half ^ 1) * 128 + rt])), f = ex2(M - M1);
+                        sum.rise(M1 - M);
+                        M = M1;
+                        if (started) {
+#pragma unroll 1
+                            for (int q = 0; q < D / 2; q += 16) {
+                                uint32_t o[16];
+                                tc::tmem_ld16_nowait(col_o + q, o);
+                                tc::tmem_ld_wait();
+#pragma unroll
+                                for (int x = 0; x < 16; ++x) o[x] = __float_as_uint(__uint_as_float(o[x]) * f);
+                                tc::tmem_st16_nowait(col_o + q, o);
+                            }
+                        }
+                    }
+                    Sum own = {0.0f, 0.0f};
+                    const float off = most == -INFINITY ? 0.0f : M - kHeadroom - e0 - most;
+                    if (!(fabsf(off) <= kApart)) own.x = rintf(off);
+                    const float d = kHeadroom - M + e0 + own.x;
+                    uint32_t w[32];
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) {
+                        uint32_t v[16];
+                        const float a = logits(q, v), dw = f2[q].y - M + kHeadroom;
+                        const uint64_t ff = pack2(a, a), dd = pack2(d, d), ww = pack2(dw, dw);
+                        uint64_t acc = 0;
+#pragma unroll
                         for (int x = 0; x < 16; x += 2) {
-                            m = x ? max3(m, __uint_as_float(v[x]), __uint_as_float(v[x + 1])) : fmaxf(m, __uint_as_float(v[1]));
                             const float2 z = unpack2(fma2(pack2(__uint_as_float(v[x]), __uint_as_float(v[x + 1])), ff, dd));
-                            const float2 e = make_float2(ex2(z.x), ex2(z.y));
-                            sum = add2(sum, pack2(e.x, e.y));
-                            const __half2 h = __floats2half2_rn(e.x, e.y);
+                            acc = add2(acc, pack2(ex2(z.x), ex2(z.y)));
+                        }
+                        const float2 s2 = unpack2(acc);
+                        own.l += s2.x + s2.y;
+                        if (__all_sync(0xFFFFFFFFu, most + dw < -25.5f)) {    // zeros in fp16: no need to work them out
+#pragma unroll
+                            for (int x = 0; x < 8; ++x) w[q * 8 + x] = 0;
+                            continue;
+                        }
+#pragma unroll
+                        for (int x = 0; x < 16; x += 2) {
+                            const float2 z = unpack2(fma2(pack2(__uint_as_float(v[x]), __uint_as_float(v[x + 1])), ff, ww));
+                            const __half2 h = __floats2half2_rn(ex2(z.x), ex2(z.y));
                             memcpy(&w[q * 8 + x / 2], &h, 4);
                         }
-                        top = fmaxf(top, m * a + f.y);
-                        // back from 2^(z + log2 vs - M + 8) to 2^(z + e0 - M + 8), exactly
-                        const float2 s2 = unpack2(sum);
-                        l1 += (s2.x + s2.y) * g1[q];
                     }
-                    // all of S is in registers from here: the weights may go over it
-                    if (agree(ok && !(top > M + kLazy))) break;
-                    xch[half * 128 + rt] = top;
-                    ok = agree(ok);
+                    ok = agree(ok);                // S has been read, and the other half's maximum
                     if (!ok) break;
-                    const float M1 = fmaxf(M, fmaxf(top, xch[(half ^ 1) * 128 + rt])), f = ex2(M - M1);
-                    l *= f;
-                    M = M1;
-                    if (started) {
-#pragma unroll 1
-                        for (int q = 0; q < D / 2; q += 16) {
-                            uint32_t o[16];
-                            tc::tmem_ld16_nowait(col_o + q, o);
-                            tc::tmem_ld_wait();
-#pragma unroll
-                            for (int x = 0; x < 16; ++x) o[x] = __float_as_uint(__uint_as_float(o[x]) * f);
-                            tc::tmem_st16_nowait(col_o + q, o);
-                        }
-                    }
-                    ok = agree(ok);            // the other half has read this one's maximum
-                    if (!ok) break;
+                    started = true;
+                    tc::tmem_st16_nowait(col_s + half * 32, w);
+                    tc::tmem_st16_nowait(col_s + half * 32 + 16, w + 16);
+                    tc::tmem_st_wait();
+                    tc::fence_before_sync();
+                    tc::mbar_arrive(bars + kP + t);
+                    sum.add(own);
+                    wide = !agree(ok && sum.x == 0.0f);
                 }
-                if (!ok) break;
-                l += l1;
-                started = true;
-                tc::tmem_st16_nowait(col_s + half * 32, w);
-                tc::tmem_st16_nowait(col_s + half * 32 + 16, w + 16);
-                tc::tmem_st_wait();
-                tc::fence_before_sync();
-                tc::mbar_arrive(bars + kP + t);
+                ++i, ++tile;
             }
             // ---- the outputs, half the channels
             ok = ok && wait_warp(kO, o_phase);
             o_phase ^= 1;
             tc::fence_after_sync();
-            xch[half * 128 + rt] = l;
-            ok = agree(ok);
-            l = half ? xch[rt] + l : l + xch[128 + rt];
+            {   // the row's other half's sum; and its unit, where there are any but 2^e0
+                xch[half * 128 + rt] = sum.l;
+                const bool plain = agree(ok && sum.x == 0.0f);
+                Sum other = {xch[(half ^ 1) * 128 + rt], 0.0f};
+                if (!plain) {
+                    ok = agree(ok);
+                    xch[half * 128 + rt] = sum.x;
+                    ok = agree(ok);
+                    other.x = xch[(half ^ 1) * 128 + rt];
+                }
+                sum.add(other);
+            }
             Cursor cur = item();
             const int row = dual ? rt : t * kTileRows + rt;
             const bool mine = row < cur.rows;
@@ -556,18 +718,31 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv8_prefill(const __grid_consta
                         for (int x = 0; x < 16; ++x)
                             odd[(half * (D / 2) + q + x) * 128 + rt] = started ? __uint_as_float(o[x]) : 0.0f;
                     }
-                    if (half == 0) stats[rt] = M, stats[128 + rt] = l;
+                    if (half == 0) stats[rt] = M, stats[128 + rt] = sum.l;
                 }
-                ok = both_tiles(ok);
+                const bool plain = both_tiles(ok && (t == 0 || sum.x == 0.0f));
+                const float M1 = stats[rt];
+                Sum other = {stats[128 + rt], 0.0f};
+                if (!plain) {
+                    ok = both_tiles(ok);
+                    if (t == 1 && half == 0) stats[rt] = sum.x;
+                    ok = both_tiles(ok);
+                    other.x = stats[rt];
+                }
                 if (t == 0) {
-                    const float M1 = stats[rt], l2 = stats[128 + rt], top = fmaxf(M, M1);
+                    const float top = fmaxf(M, M1);
                     f0 = ex2(M - top);
                     f1 = ex2(M1 - top);
-                    l = l * f0 + l2 * f1;
+                    sum.rise(top - M);
+                    other.rise(top - M1);
+                    sum.add(other);
                     M = top;
                 }
             }
-            const float f = l == 0.0f ? 0.0f : exp2_int((int)e0) / l;
+            if (!(fabsf(e0 + sum.x) <= 100.0f)) sum.normalise();
+            // outputs: O 2^e / l, -136 < e <= 120, in two factors, of which the first stays a normal number
+            const float l = sum.l, e = e0 + sum.x, scale = ex2(fminf(e + 100.0f, 0.0f));
+            const float f = l == 0.0f ? 0.0f : ex2(fmaxf(e, -100.0f)) / l;
             if (ok && (!dual || t == 0)) {
                 const float* odd = reinterpret_cast<const float*>(smem + S::q);
                 const uint32_t live = __ballot_sync(0xFFFFFFFFu, mine);
@@ -581,6 +756,10 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv8_prefill(const __grid_consta
 #pragma unroll
                         for (int x = 0; x < 32; ++x)
                             r[x] = __float_as_uint(__uint_as_float(r[x]) * f0 + odd[(ch + x) * 128 + rt] * f1);
+                    }
+                    if (__any_sync(0xFFFFFFFFu, scale != 1.0f)) {
+#pragma unroll
+                        for (int x = 0; x < 32; ++x) r[x] = __float_as_uint(__uint_as_float(r[x]) * (whole ? scale : 1.0f));
                     }
                     if (whole) {
                         // through shared memory, two rows of 64 bytes in 128, so that they leave by lines: over the
@@ -629,10 +808,10 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv8_prefill(const __grid_consta
                 if (mine && half == 0) {
                     if (whole) {
                         if (p.a.lse)
-                            p.a.lse[at] = l == 0.0f ? -INFINITY : (M - e0 - kHeadroom + log2f(l)) * 0.6931471805599453f;
+                            p.a.lse[at] = l == 0.0f ? -INFINITY : (M - e - kHeadroom + log2f(l)) * 0.6931471805599453f;
                     } else {
                         float* s3 = part + Part<D>::kStats + row * 3;
-                        s3[0] = l == 0.0f ? kNone : M - e0 - kHeadroom;
+                        s3[0] = l == 0.0f ? kNone : M - e - kHeadroom;
                         s3[1] = l;
                         s3[2] = M - kHeadroom;
                     }
@@ -708,6 +887,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv8_prefill(const __grid_consta
             uint32_t issued = 0, steps = (uint32_t)piece_steps;
             int phys = -1, lim = 0, h = 0, e0 = 0;  // lim: positions before the sequence's end, and (<< 8) how many are not looked up
             bool fresh = true, item_ends = true;    // the tile is the first of its item in this piece
+            bool high = false;                      // a tile of the item had a value scale far above the sums' unit
             auto look = [&](bool there) {    // lane x < 8: the block of positions 16 x .. of the tile at `cur`
                 phys = -1;
                 fresh = item_ends;
@@ -747,22 +927,22 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv8_prefill(const __grid_consta
                 for (int kv = 0; kv < 2 && ok; ++kv) {
                     if (tile >= 1) ok = wait_warp(kLEmpty + kv, (tile - 1) & 1);
                     if (!ok) break;
-                    if (kv == 0) {
-                        // a block of zero values has the least scale: any will do, and the sums' own is exact
-                        int ev = (int)(__float_as_uint(vs) >> 23) - 127;
-                        if (ev == -120) ev = e0;
-                        const int de = e0 - ev;
-                        if (lane < 8) {
-                            sc[(tile & 7) * 8 + lane] = make_float2(ks, (float)ev);
-                            sg[(tile & 7) * 8 + lane] = exp2_int(de < -126 ? -126 : (de > 126 ? 126 : de));
-                        }
-                        if (lane == 0) lims[tile & 7] = now_lim;
-                        __syncwarp();
-                    }
-                    if (lane == 0) tc::mbar_arrive_expect_tx(bars + kLFull + kv, n * box * D);
+                    if (lane == 0) tc::mbar_expect_tx(bars + kLFull + kv, n * box * D);
                     __syncwarp();
                     if (copy)
                         tc::tma_load_2d(smem + S::codes + kv * kPos * D + lane * box * D, kv ? &vmap : &kmap, 0, row, bars + kLFull + kv);
+                    if (kv == 0) {     // the scales, while the codes are under way
+                        const int ev = now >= 0 ? (int)(__float_as_uint(vs) >> 23) - 127 : e0;
+                        high = (high && !first) || __any_sync(0xFFFFFFFFu, ev - e0 > kSpread);
+                        const bool apart = high || __any_sync(0xFFFFFFFFu, e0 - ev > kSpread);
+                        if (lane < 8) {
+                            sc[(tile & 7) * 8 + lane] = make_float2(ks, (float)ev);
+                            sg[(tile & 7) * 8 + lane] = apart ? 0.0f : exp2_int(e0 - ev);
+                        }
+                        if (lane == 0) lims[tile & 7] = now_lim;
+                    }
+                    __syncwarp();
+                    if (lane == 0) tc::mbar_arrive(bars + kLFull + kv);
                     __syncwarp();
                     ++issued;
                 }
@@ -896,14 +1076,16 @@ template <int D>
 __device__ __forceinline__ void store_row(const Params& p, int b, int h, int row, int q4, const float4& s, float m, float M, float l) {
     const int j = row / p.G, g = row - j * p.G;
     const int64_t at = ((int64_t)b * p.a.q.T + j) * p.a.q.H + h * p.G + g;
-    const float f = l == 0.0f ? 0.0f : ex2(M - m) / l;
+    // 2^(M - m) / l in two factors: the first stays a normal number
+    const float f = l == 0.0f ? 0.0f : ex2(fmaxf(M - m, -100.0f)) / l, f2 = ex2(fminf(M - m + 100.0f, 0.0f));
+    const float x = s.x * f2 * f, y = s.y * f2 * f, z = s.z * f2 * f, u = s.w * f2 * f;
     uint32_t w[2];
     if (p.a.q.is_bf16) {
-        const __nv_bfloat162 a = __floats2bfloat162_rn(s.x * f, s.y * f), b2 = __floats2bfloat162_rn(s.z * f, s.w * f);
+        const __nv_bfloat162 a = __floats2bfloat162_rn(x, y), b2 = __floats2bfloat162_rn(z, u);
         memcpy(&w[0], &a, 4);
         memcpy(&w[1], &b2, 4);
     } else {
-        const __half2 a = __floats2half2_rn(s.x * f, s.y * f), b2 = __floats2half2_rn(s.z * f, s.w * f);
+        const __half2 a = __floats2half2_rn(x, y), b2 = __floats2half2_rn(z, u);
         memcpy(&w[0], &a, 4);
         memcpy(&w[1], &b2, 4);
     }
