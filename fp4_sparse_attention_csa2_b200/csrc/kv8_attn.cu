@@ -242,8 +242,16 @@ struct Part {
     static constexpr int kStats = 16 * D, kDesc = kStats + 16 * 3, kFloats = kDesc + 16;
 };
 
-// Four adjacent outputs x * f, rounded once to the query's type.
-__device__ __forceinline__ void store_out(void* out, int is_bf16, int64_t at, const float* x, float f) {
+// Four adjacent outputs x * 2^(M - m - 8) / l, rounded once to the query's type.
+// M - m is as low as the least value scale, -120, and 2^-128 / l nothing in fp32:
+// there the power of two goes in two parts.
+__device__ __forceinline__ void store_out(void* out, int is_bf16, int64_t at, float* x, float m, float l, float M) {
+    constexpr float kLow = -100.0f;
+    const float e = M - m - kHeadroom, f = l == 0.0f ? 0.0f : ex2(fmaxf(e, kLow)) / l;
+    if (e < kLow) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) x[i] *= ex2(e - kLow);
+    }
     uint32_t w[2];
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
@@ -831,8 +839,7 @@ __global__ void __launch_bounds__(kThreads, kPerSm) k_kv8_attn(const __grid_cons
                     if (whole) {
                         const int2 jg = work.token(cur, row);
                         const int64_t at = ((int64_t)cur.b * T + jg.x) * H + cur.h * G + jg.y;
-                        store_out(p.a.out, p.a.q.is_bf16, at * D + ch, y,
-                                  lr == 0.0f ? 0.0f : ex2(Mr - mr - kHeadroom) / lr);
+                        store_out(p.a.out, p.a.q.is_bf16, at * D + ch, y, mr, lr, Mr);
                         if (p.a.lse && first) p.a.lse[at] = lr == 0.0f ? -INFINITY : (mr + log2f(lr)) * 0.6931471805599453f;
                     } else {
                         *reinterpret_cast<float4*>(part + row * D + ch) = make_float4(y[0], y[1], y[2], y[3]);
@@ -925,7 +932,7 @@ __global__ void __launch_bounds__(4 * D) k_kv8_combine(const __grid_constant__ P
     k.rt = desc[2];
     const int2 jg = work.token(k, row);
     const int64_t at = ((int64_t)desc[0] * p.a.q.T + jg.x) * p.a.q.H + desc[1] * p.G + jg.y;
-    store_out(p.a.out, p.a.q.is_bf16, at * D + q4 * 4, y, l == 0.0f ? 0.0f : ex2(M - m - kHeadroom) / l);
+    store_out(p.a.out, p.a.q.is_bf16, at * D + q4 * 4, y, m, l, M);
     if (p.a.lse && q4 == 0) p.a.lse[at] = l == 0.0f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
 }
 
@@ -1025,7 +1032,7 @@ __global__ void __launch_bounds__(kMergeWarps * 32) k_kv8_combine_few(const __gr
     k.rt = found[4];
     const int2 jg = work.token(k, row);
     const int64_t at = ((int64_t)found[2] * p.a.q.T + jg.x) * p.a.q.H + found[3] * p.G + jg.y;
-    store_out(p.a.out, p.a.q.is_bf16, at * D + q4 * 4, y, l == 0.0f ? 0.0f : ex2(M - m - kHeadroom) / l);
+    store_out(p.a.out, p.a.q.is_bf16, at * D + q4 * 4, y, m, l, M);
     if (p.a.lse && q4 == 0) p.a.lse[at] = l == 0.0f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
 }
 

@@ -88,7 +88,8 @@ APART = [[2.0 ** 60, 2.0 ** -80], [2.0 ** -80, 2.0 ** 60], [2.0 ** 100, 1.0, 2.0
 
 
 @pytest.mark.parametrize("mags", TINY)
-@pytest.mark.parametrize("heads,G,D,bs,T", [(1, 4, 128, 64, 64), (2, 4, 64, 16, 20), (1, 8, 128, 128, 40)])
+@pytest.mark.parametrize("heads,G,D,bs,T", [(1, 4, 128, 64, 1), (2, 8, 64, 16, 2), (1, 4, 128, 64, 64),
+                                            (2, 4, 64, 16, 20), (1, 8, 128, 128, 40)])
 def test_least_value_scale(mags, heads, G, D, bs, T):
     lens = [300, 257]
     dev, r = with_values(heads, D, bs, lens, mags, room=T * G > 16)
@@ -96,7 +97,8 @@ def test_least_value_scale(mags, heads, G, D, bs, T):
 
 
 @pytest.mark.parametrize("mags", APART)
-@pytest.mark.parametrize("heads,G,D,bs,T", [(1, 4, 128, 32, 64), (2, 4, 64, 16, 20), (1, 8, 128, 128, 40)])
+@pytest.mark.parametrize("heads,G,D,bs,T", [(1, 4, 128, 64, 1), (2, 8, 64, 16, 2), (1, 4, 128, 32, 64),
+                                            (2, 4, 64, 16, 20), (1, 8, 128, 128, 40)])
 def test_value_scales_far_apart(mags, heads, G, D, bs, T):
     lens = [700, 513]
     dev, r = with_values(heads, D, bs, lens, mags, room=T * G > 16)
@@ -113,7 +115,7 @@ def test_scales_in_items_of_many_steps(mags, D, T, G):
     check(dev, r, lens, T, 8 * G)
 
 
-@pytest.mark.parametrize("T,G,room", [(60, 4, True)])
+@pytest.mark.parametrize("T,G,room", [(1, 8, False), (60, 4, True)])
 def test_least_scale_over_many_pieces(T, G, room):
     # one item cut into pieces that a second launch merges
     for mags in ([1e-35], [1e-35, 2.0 ** -7, 0.0], [2.0 ** 70, 2.0 ** -70]):
