@@ -130,12 +130,12 @@ csa2_status csa2_kv8_append(const csa2_kv8_cache* cache, const void* k_new, cons
     CSA2_RANGE("csa2_kv8_append");
     const csa2_status s = check_cache(cache);
     if (s != CSA2_OK) return s;
+    if (T == 0) return CSA2_OK;   // nothing to append, and tensors without rows have no address
     if (!k_new || !v_new || !start_pos || !aligned(k_new, 16) || !aligned(v_new, 16) || !aligned(start_pos, 4) ||
         !aligned(n_new, 4) || !aligned(ws, 16))
         return CSA2_ERR_INVALID_ARG;
     if (dtype != CSA2_BF16 && dtype != CSA2_F16 && dtype != CSA2_F32) return CSA2_ERR_INVALID_ARG;
     if (stride_b % 8 || stride_t % 8 || T < 0 || T > 1 << 30) return CSA2_ERR_INVALID_ARG;
-    if (T == 0) return CSA2_OK;
     return cuda_status(launch_kv8_append(dev_kv8(cache), k_new, v_new, dtype, stride_b, stride_t, start_pos, n_new, T,
                                          static_cast<uint32_t*>(ws), static_cast<cudaStream_t>(stream)));
 }
@@ -145,12 +145,12 @@ csa2_status csa2_kv8_read(const csa2_kv8_cache* cache, const int32_t* start_pos,
     CSA2_RANGE("csa2_kv8_read");
     const csa2_status s = check_cache(cache);
     if (s != CSA2_OK) return s;
+    if (T == 0) return CSA2_OK;
     if (!k_out || !v_out || !start_pos || !aligned(k_out, 32) || !aligned(v_out, 32) || !aligned(start_pos, 4) ||
         !aligned(n_rows, 4) || !aligned(ws, 16))
         return CSA2_ERR_INVALID_ARG;
     if (dtype != CSA2_BF16 && dtype != CSA2_F16 && dtype != CSA2_F32) return CSA2_ERR_INVALID_ARG;
     if (T < 0 || T > 1 << 30) return CSA2_ERR_INVALID_ARG;
-    if (T == 0) return CSA2_OK;
     return cuda_status(launch_kv8_read(dev_kv8(cache), start_pos, n_rows, T, k_out, v_out, dtype,
                                        static_cast<uint32_t*>(ws), static_cast<cudaStream_t>(stream)));
 }

@@ -580,7 +580,7 @@ CSA2_API size_t csa2_kv8_workspace_bytes(const csa2_kv8_cache* cache, int T, int
  * CSA2_ERR_NONFINITE in ws; positions outside the cache are skipped and set
  * CSA2_ERR_DEVICE_BOUNDS (ws nullable, only its status word is used).
  * (T + block_size) rounded up to blocks times n_kv_heads is the grid: T up to
- * 2^30.
+ * 2^30.  T == 0: nothing happens, whatever the other arguments but the cache are.
  */
 CSA2_API csa2_status csa2_kv8_append(const csa2_kv8_cache* cache, const void* k_new, const void* v_new,
                                      csa2_dtype dtype, int64_t stride_b, int64_t stride_t, int T,
@@ -590,7 +590,8 @@ CSA2_API csa2_status csa2_kv8_append(const csa2_kv8_cache* cache, const void* k_
  * Rows back as values: k_out, v_out [batch][T][n_kv_heads][head_dim] (dense, of
  * dtype) <- value(code) * scale of positions start_pos[b] + j, j < n_rows[b],
  * rounded once; k_out and v_out 32-byte aligned.  A position outside the cache
- * is written as zeros and sets CSA2_ERR_DEVICE_BOUNDS in ws (nullable).
+ * is written as zeros and sets CSA2_ERR_DEVICE_BOUNDS in ws (nullable).  T == 0:
+ * nothing happens.
  */
 CSA2_API csa2_status csa2_kv8_read(const csa2_kv8_cache* cache, const int32_t* start_pos, const int32_t* n_rows,
                                    int T, void* k_out, void* v_out, csa2_dtype dtype, void* ws, void* stream);

@@ -76,6 +76,15 @@ def test_nothing_to_do_launches_nothing(lib):
     assert lib.csa2_kv8_read(c, 0x3000, None, 0, 0x1000, 0x2000, csa2.BF16, None, None) == csa2.OK
 
 
+def test_no_rows_need_no_rows_address(lib):
+    # what a tensor without elements has for an address is null
+    c = ctypes.byref(fake())
+    assert lib.csa2_kv8_append(c, None, None, csa2.BF16, 512, 512, 0, 0x3000, None, None, None) == csa2.OK
+    assert lib.csa2_kv8_read(c, 0x3000, None, 0, None, None, csa2.BF16, None, None) == csa2.OK
+    assert lib.csa2_kv8_append(ctypes.byref(fake(batch=0)), None, None, csa2.BF16, 512, 512, 0, 0x3000, None, None,
+                               None) == csa2.ERR_INVALID_ARG
+
+
 @pytest.mark.parametrize("kw", [
     dict(q=None), dict(q=0x1008), dict(dt=csa2.F32), dict(dt=csa2.E4M3), dict(sb=4), dict(st=2), dict(T=0), dict(H=0),
     dict(H=30), dict(H=2), dict(n=0x4002), dict(out=None), dict(out=0x2008), dict(lse=0x3002), dict(ws=None),
