@@ -514,9 +514,7 @@ class KV8Cache:
         n_blocks, heads, bs, dim = k.shape
         batch = seq_lens.numel()
         if table is not None:
-            max_blocks = table.shape[1] if max_blocks is None else max_blocks
-            if table.dtype != torch.int32 or tuple(table.shape) != (batch, max_blocks):
-                raise ValueError("block_table is int32 [batch, max_blocks]")
+            max_blocks = table.shape[-1] if max_blocks is None else max_blocks
         elif max_blocks is None:
             max_blocks = n_blocks // batch
         for t, dt, shape, what in ((k, torch.uint8, (n_blocks, heads, bs, dim), "k_codes"),
@@ -524,7 +522,8 @@ class KV8Cache:
                                    (ks, torch.float32, (n_blocks, heads), "k_scale"),
                                    (vs, torch.float32, (n_blocks, heads), "v_scale"),
                                    (kb, torch.uint8, (n_blocks, heads, 2, dim), "k_bounds"),
-                                   (seq_lens, torch.int32, (batch,), "seq_lens")):
+                                   (seq_lens, torch.int32, (batch,), "seq_lens"),
+                                   (table, torch.int32, (batch, max_blocks), "block_table")):
             if t is not None and (t.dtype != dt or tuple(t.shape) != shape):
                 raise ValueError("%s is %s %s; got %s %s" % (what, dt, shape, t.dtype, tuple(t.shape)))
             if t is not None and t.device != k.device:

@@ -180,3 +180,41 @@ def test_binding_row_checks():
         csa2._kv8_ptr(c, torch.zeros(2, 2), torch.float32, (2, 2), "x")
     with pytest.raises(ValueError):
         csa2._kv8_rows(c, rows[:, :, :2], 2, "q")
+
+
+class _On:
+    """A tensor on a GPU as far as the checks of KV8Cache look at one: type, shape, device, address."""
+    is_cuda = True
+
+    def __init__(self, shape, dtype, device=0, addr=0x10000):
+        self.shape, self.dtype, self.device, self.addr = torch.Size(shape), dtype, torch.device("cuda", device), addr
+
+    def numel(self):
+        return self.shape.numel()
+
+    def get_device(self):
+        return self.device.index
+
+    def is_contiguous(self):
+        return True
+
+    def data_ptr(self):
+        return self.addr
+
+
+def parts(**kw):
+    """The tensors of a cache of 2 sequences, 8 blocks."""
+    d = dict(k_codes=_On((8, 2, 16, 64), torch.uint8), v_codes=_On((8, 2, 16, 64), torch.uint8),
+             k_scale=_On((8, 2), torch.float32), v_scale=_On((8, 2), torch.float32), seq_lens=_On((2,), torch.int32),
+             k_bounds=_On((8, 2, 2, 64), torch.uint8), block_table=_On((2, 4), torch.int32))
+    d.update(kw)
+    return d
+
+
+def test_cache_on_two_devices_is_refused():
+    assert csa2.KV8Cache.wrap(**parts()).c.max_blocks == 4
+    for name, t in parts().items():
+        if name == "k_codes":
+            continue
+        with pytest.raises(ValueError):
+            csa2.KV8Cache.wrap(**parts(**{name: _On(t.shape, t.dtype, device=1)}))
