@@ -579,11 +579,13 @@ def _kv8_rows(cache, t, heads, what):
 
 
 def _kv8_ws(cache, ws):
+    """Address and bytes of a workspace; append and read use its status word alone."""
     if ws is None:
-        return None
-    if ws.get_device() != cache.index or not ws.is_contiguous():
-        raise ValueError("the workspace is a contiguous tensor on the cache's device")
-    return ws.data_ptr()
+        raise ValueError("a workspace is needed (kv8_workspace_bytes)")
+    n = ws.nbytes
+    if n < 4 or ws.get_device() != cache.index or not ws.is_contiguous():
+        raise ValueError("the workspace is a contiguous tensor of 4 bytes or more on the cache's device")
+    return ws.data_ptr(), n
 
 
 def _kv8_call(cache, stream, what, fn, *args):
@@ -623,7 +625,7 @@ def kv8_append(cache, k_new, v_new, start_pos, n_new=None, ws=None, stream=None)
         raise ValueError("k_new and v_new must have equal strides")
     _kv8_call(cache, stream, "kv8_append", lib().csa2_kv8_append, kp, vp, dt, sb, st, k_new.shape[1],
               _kv8_ptr(cache, start_pos, torch.int32, B, "start_pos"), _kv8_ptr(cache, n_new, torch.int32, B, "n_new"),
-              _kv8_ws(cache, ws))
+              None if ws is None else _kv8_ws(cache, ws)[0])
 
 
 def kv8_read(cache, start_pos, k_out, v_out, n_rows=None, ws=None, stream=None):
@@ -637,7 +639,7 @@ def kv8_read(cache, start_pos, k_out, v_out, n_rows=None, ws=None, stream=None):
               _kv8_ptr(cache, start_pos, torch.int32, B, "start_pos"),
               _kv8_ptr(cache, n_rows, torch.int32, B, "n_rows"), shape[1],
               _kv8_ptr(cache, k_out, k_out.dtype, shape, "k_out"), _kv8_ptr(cache, v_out, k_out.dtype, shape, "v_out"),
-              dt, _kv8_ws(cache, ws))
+              dt, None if ws is None else _kv8_ws(cache, ws)[0])
 
 
 _KV8_QUERY_DTYPES = {torch.bfloat16: BF16, torch.float16: F16}
@@ -659,7 +661,7 @@ def _kv8_query(cache, q, n_q):
 def _kv8_outputs(cache, q, out, lse, ws):
     shape = q.shape
     return (_kv8_ptr(cache, out, q.dtype, shape, "out"),
-            None if lse is None else _kv8_ptr(cache, lse, torch.float32, shape[:3], "lse"), _kv8_ws(cache, ws), ws.nbytes)
+            None if lse is None else _kv8_ptr(cache, lse, torch.float32, shape[:3], "lse"), *_kv8_ws(cache, ws))
 
 
 def kv8_attn(cache, q, out, ws, lse=None, window=0, n_q=None, sm_scale=0.0, stream=None):
@@ -678,7 +680,7 @@ def kv8_select_blocks(cache, q, block_idx, ws, n_first=0, n_recent=1, n_q=None, 
     args, n_sel = _kv8_query(cache, q, n_q), block_idx.shape[-1]
     _kv8_call(cache, stream, "kv8_select_blocks", lib().csa2_kv8_select_blocks, *args, n_sel, n_first, n_recent,
               _kv8_ptr(cache, block_idx, torch.int32, (cache.batch, args[4], cache.n_kv_heads, n_sel), "block_idx"),
-              _kv8_ws(cache, ws), ws.nbytes)
+              *_kv8_ws(cache, ws))
 
 
 def kv8_block_attn(cache, q, block_idx, out, ws, lse=None, n_q=None, sm_scale=0.0, stream=None):

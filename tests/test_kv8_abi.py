@@ -218,3 +218,25 @@ def test_cache_on_two_devices_is_refused():
             continue
         with pytest.raises(ValueError):
             csa2.KV8Cache.wrap(**parts(**{name: _On(t.shape, t.dtype, device=1)}))
+
+
+class _Host(torch.Tensor):
+    """A host tensor that says it is on the GPU: only its address would be taken."""
+    def get_device(self):
+        return 0
+
+
+def test_query_calls_want_a_workspace_and_all_calls_one_with_a_status_word(lib):
+    c = csa2.KV8Cache.wrap(**parts())
+    z = lambda *s, dt=torch.bfloat16: torch.zeros(s, dtype=dt).as_subclass(_Host)
+    q, idx, rows, start = z(2, 1, 4, 64), z(2, 1, 2, 3, dt=torch.int32), z(2, 1, 2, 64), z(2, dt=torch.int32)
+    calls = [lambda ws: csa2.kv8_attn(c, q, q, ws), lambda ws: csa2.kv8_select_blocks(c, q, idx, ws),
+             lambda ws: csa2.kv8_block_attn(c, q, idx, q, ws)]
+    for call in calls:
+        with pytest.raises(ValueError, match="workspace"):
+            call(None)
+    calls += [lambda ws: csa2.kv8_append(c, rows, rows, start, ws=ws), lambda ws: csa2.kv8_read(c, start, rows, rows, ws=ws)]
+    for call in calls:
+        for small in (z(0, dt=torch.uint8), z(3, dt=torch.uint8)):    # a status word is four bytes
+            with pytest.raises(ValueError, match="workspace"):
+                call(small)
