@@ -486,7 +486,18 @@ class KV8Cache:
     block table [batch, max_blocks] (None: contiguous) and seq_lens [batch],
     all on one device.  seq_lens counts the rows of the current call; the
     caller advances it (`cache.seq_lens += n`) and nothing in the library
-    changes it."""
+    changes it.  Another tensor put in place of one of these (a longer block
+    table, say) is checked and used from then on."""
+
+    _TENSORS = ("k", "v", "k_scale", "v_scale", "seq_lens", "k_bounds", "block_table")
+
+    def __setattr__(self, name, value):
+        # the library is handed addresses: a new tensor means new ones
+        if name not in self._TENSORS or self.__dict__.get(name) is value:
+            return object.__setattr__(self, name, value)
+        parts = {n: getattr(self, n) for n in self._TENSORS}
+        parts[name] = value
+        self._set(*parts.values(), None if name == "block_table" and value is not None else self.max_blocks)
 
     def __init__(self, batch, n_kv_heads, head_dim, max_blocks, seq_lens, block_size=64, n_blocks=None,
                  block_table=None, bounds=True, device="cuda"):
@@ -528,13 +539,13 @@ class KV8Cache:
                 raise ValueError("%s is %s %s; got %s %s" % (what, dt, shape, t.dtype, tuple(t.shape)))
             if t is not None and t.device != k.device:
                 raise ValueError("the cache's tensors live on one device")
-        self.k, self.v, self.k_scale, self.v_scale, self.k_bounds = k, v, ks, vs, kb
-        self.seq_lens, self.block_table = seq_lens, table
+        c = csa2_kv8_cache(_addr(k), _addr(v), _addr(ks), _addr(vs), _addr(kb), _addr(table), _addr(seq_lens),
+                           batch, max_blocks, bs, heads, dim, n_blocks)
+        self.__dict__.update(zip(self._TENSORS, (k, v, ks, vs, seq_lens, kb, table)))
         self.batch, self.max_blocks, self.block_size, self.n_kv_heads, self.head_dim = batch, max_blocks, bs, heads, dim
         self.device, self.index = k.device, k.get_device()
-        self.c = csa2_kv8_cache(_addr(k), _addr(v), _addr(ks), _addr(vs), _addr(kb), _addr(table), _addr(seq_lens),
-                                batch, max_blocks, bs, heads, dim, n_blocks)
-        self.ref = ctypes.byref(self.c)
+        self.c = c
+        self.ref = ctypes.byref(c)
 
 
 # A decode step makes a few of these calls per layer, each a few microseconds on

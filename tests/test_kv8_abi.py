@@ -240,3 +240,22 @@ def test_query_calls_want_a_workspace_and_all_calls_one_with_a_status_word(lib):
         for small in (z(0, dt=torch.uint8), z(3, dt=torch.uint8)):    # a status word is four bytes
             with pytest.raises(ValueError, match="workspace"):
                 call(small)
+
+
+def test_a_tensor_put_in_place_of_a_caches_own_is_the_one_that_calls_use():
+    c = csa2.KV8Cache.wrap(**parts())
+    lens, table = _On((2,), torch.int32, addr=0x20000), _On((2, 6), torch.int32, addr=0x30000)
+    c.seq_lens = lens                                          # as in cache.seq_lens = cache.seq_lens + 1
+    assert c.c.seq_lens == 0x20000 and c.seq_lens is lens and c.ref._obj is c.c
+    c.block_table = table                                      # a wider table: sequences may grow further
+    assert (c.c.block_table, c.c.max_blocks, c.max_blocks) == (0x30000, 6, 6) and c.c.seq_lens == 0x20000
+    c.seq_lens = lens                                          # the same again, as += leaves it
+    assert c.c.seq_lens == 0x20000
+    c.k_bounds = None
+    assert c.c.k_bounds is None and c.c.k_codes == 0x10000
+    for name, bad in (("seq_lens", _On((2,), torch.int64)), ("seq_lens", _On((2,), torch.int32, device=1)),
+                      ("block_table", _On((3, 4), torch.int32)), ("v", _On((8, 2, 16, 128), torch.uint8)),
+                      ("seq_lens", torch.zeros(2, dtype=torch.int32))):
+        with pytest.raises(ValueError):
+            setattr(c, name, bad)
+        assert c.seq_lens is lens and c.c.seq_lens == 0x20000 and c.block_table is table and c.max_blocks == 6
