@@ -165,7 +165,7 @@ __global__ void __launch_bounds__(kThreads) k_kv8_append(DevKv8 c, const T* k_ne
     const int64_t start = __ldg(start_pos + b);
     if (n == 0) return;
     if (start < 0 || start + n > cap) flag(status, kStatusBounds);
-    if (start < 0) return;
+    if (start < 0) return;   // none of the rows: where such a call's rows belong is not to be guessed
     const int64_t end = start + n < cap ? start + n : cap;
     const int64_t lb = (start >> c.bs_log2) + blockIdx.x, pos0 = lb << c.bs_log2;
     if (pos0 >= end) return;

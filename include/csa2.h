@@ -577,7 +577,8 @@ CSA2_API size_t csa2_kv8_workspace_bytes(const csa2_kv8_cache* cache, int T, int
  * positions before start_pos; what it held behind them is overwritten or left.
  * The call does not change seq_lens.  Rows must be finite: an infinity is
  * stored as +-448 s, a NaN as 0, neither counts for s, and either sets
- * CSA2_ERR_NONFINITE in ws; positions outside the cache are skipped and set
+ * CSA2_ERR_NONFINITE in ws; positions behind the cache's last are skipped, and
+ * all rows of a sequence whose start_pos is negative, and either sets
  * CSA2_ERR_DEVICE_BOUNDS (ws nullable, only its status word is used).
  * (T + block_size) rounded up to blocks times n_kv_heads is the grid: T up to
  * 2^30.  T == 0: nothing happens, whatever the other arguments but the cache are.
