@@ -74,8 +74,9 @@ __device__ __forceinline__ int kv8_block(const DevKv8& c, int b, int lb) {
 
 // The scale of a block whose greatest finite magnitude is amax: the least 2^e,
 // -120 <= e <= 120, with amax <= 448 * 2^e (448 = 1.75 * 2^8), from amax's own
-// exponent and mantissa.  The limits keep 2^e, 2^-e and code * 2^e in fp32's
-// normal range.
+// exponent and mantissa.  The limits keep 2^e and 2^-e normal numbers in fp32,
+// and the least code times 2^e, 2^-129, a subnormal one; at the top code 256 times
+// 2^120 is infinity (rows within 3 % of fp32's greatest number).
 __device__ __forceinline__ int kv8_scale_exp(float amax) {
     const uint32_t u = __float_as_uint(amax);
     const int x = (int)(u >> 23) - 127;  // subnormal amax: x = -127, clamped below

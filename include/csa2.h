@@ -582,6 +582,8 @@ CSA2_API size_t csa2_kv8_workspace_bytes(const csa2_kv8_cache* cache, int T, int
  * CSA2_ERR_DEVICE_BOUNDS (ws nullable, only its status word is used).
  * (T + block_size) rounded up to blocks times n_kv_heads is the grid: T up to
  * 2^30.  T == 0: nothing happens, whatever the other arguments but the cache are.
+ * Values of 248 * 2^120 = 3.2965e38 and more get code 256 with the greatest scale:
+ * 2^128, which csa2_kv8_read gives back as fp32's infinity.
  */
 CSA2_API csa2_status csa2_kv8_append(const csa2_kv8_cache* cache, const void* k_new, const void* v_new,
                                      csa2_dtype dtype, int64_t stride_b, int64_t stride_t, int T,

@@ -21,6 +21,25 @@ def test_append_at_a_negative_start_drops_that_sequences_rows_alone():
     same_cache(dev, r)
 
 
+def test_rows_near_the_ends_of_fp32_read_back():
+    # 240 * 2^120 is the greatest that comes back finite; at the other end a code is worth 2^-129 and more
+    dev, r = both_caches(1, 1, 64, 16, 3)
+    x = torch.zeros(1, 33, 1, 64)
+    x[0, 0, 0, :6] = torch.tensor([3.2e38, 3.29e38, 3.2964e38, 3.4e38, -3.4e38, 1.0])
+    x[0, 16, 0, :4] = torch.tensor([1e-35, 2.0 ** -129, 2.0 ** -131, -3e-34])
+    x[0, 32, 0, :3] = torch.tensor([240.0 * 2.0 ** 120, 247.9 * 2.0 ** 120, 248.0 * 2.0 ** 120])
+    csa2.kv8_append(dev, x.cuda(), x.cuda(), i32([0]))
+    r.append(0, 0, x[0].double().numpy(), x[0].double().numpy())
+    same_cache(dev, r)
+    k, v = torch.empty_like(x).cuda(), torch.empty_like(x).cuda()
+    csa2.kv8_read(dev, i32([0]), k, v)
+    want = torch.from_numpy(r.rows(0, 0, np.arange(33))[0])[None, :, None].float()      # 256 * 2^120: infinity
+    assert torch.equal(k.cpu(), want) and torch.equal(v.cpu(), want)
+    top = 240.0 * 2.0 ** 120
+    assert k[0, 0, 0, :6].tolist()[:2] == [top, top] and bool(k[0, 0, 0, 3:5].isinf().all())
+    assert k[0, 32, 0, :3].tolist() == [top, top, float("inf")]
+
+
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16, torch.float32])
 def test_append_and_read_of_no_rows(dtype):
     dev, r = both_caches(2, 2, 64, 16, 3)
