@@ -34,12 +34,12 @@ def with_values(heads, D, bs, lens, mags, room, seed=3):
 
 
 def kernels(call):
-    """Names of the kernels that a call launches."""
+    """Names of this library's kernels that a call launches."""
     from torch.profiler import ProfilerActivity, profile
     with profile(activities=[ProfilerActivity.CUDA]) as p:
         call()
         torch.cuda.synchronize()
-    return " ".join(e.name for e in p.events())
+    return " ".join(e.name for e in p.events() if "csa2" in e.name)
 
 
 def check(dev, r, lens, T, H, seed=9):
