@@ -72,6 +72,12 @@ __device__ __forceinline__ int kv8_block(const DevKv8& c, int b, int lb) {
     return (p < 0 || p >= c.n_blocks) ? -1 : p;
 }
 
+// A value scale is used by its exponent alone; one that is no power of two (0 is
+// that of a block nobody wrote) is flagged in the debug build, like a bad index.
+__device__ __forceinline__ void kv8_check_scale(float s, uint32_t* status) {
+    if (kDebugBounds && (__float_as_uint(s) & 0x807FFFFFu)) flag(status, kStatusBounds);
+}
+
 // The scale of a block whose greatest finite magnitude is amax: the least 2^e,
 // -120 <= e <= 120, with amax <= 448 * 2^e (448 = 1.75 * 2^8), from amax's own
 // exponent and mantissa.  The limits keep 2^e and 2^-e normal numbers in fp32,

@@ -405,6 +405,8 @@ __global__ void __launch_bounds__(kThreads, kPerSm) k_kv8_attn(const __grid_cons
                     const int64_t unit = (int64_t)k.phys[i] * p.c.heads + k.h;
                     k.ks[i] = __ldg(p.c.k_scale + unit);
                     k.vs[i] = __ldg(p.c.v_scale + unit);
+                    kv8_check_scale(k.ks[i], p.a.status);
+                    kv8_check_scale(k.vs[i], p.a.status);
                 }
             }
         };

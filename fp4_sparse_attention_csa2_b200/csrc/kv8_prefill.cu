@@ -916,6 +916,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv8_prefill(const __grid_consta
                     const int64_t unit = (int64_t)now * p.c.heads + now_h;
                     ks = __ldg(p.c.k_scale + unit);
                     vs = __ldg(p.c.v_scale + unit);
+                    kv8_check_scale(ks, p.a.status);
+                    kv8_check_scale(vs, p.a.status);
                 }
                 if (first) e0 = sum_scale(__shfl_sync(0xFFFFFFFFu, vs, 0));
                 // lane x < boxes copies box x: the block of its first 16 positions

@@ -509,6 +509,9 @@ CSA2_API csa2_status csa2_lse_merge(int R, int batch, int H, int dim, const floa
  *   k_codes, v_codes  [n_blocks][n_kv_heads][block_size][head_dim] E4M3 bytes
  *   k_scale, v_scale  [n_blocks][n_kv_heads] fp32, each a power of two: a code
  *                     stands for value(code) * scale
+ *                     (attention uses a value scale's exponent alone; the
+ *                     debug build flags other scales as
+ *                     CSA2_ERR_DEVICE_BOUNDS)
  *   k_bounds          [n_blocks][n_kv_heads][2][head_dim] E4M3, or NULL: per
  *                     channel a lower and an upper bound of the block's key
  *                     codes in whole units of k_scale (csa2_kv8_select_blocks
