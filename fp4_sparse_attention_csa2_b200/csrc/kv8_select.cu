@@ -538,6 +538,12 @@ cudaError_t launch_kv8_select(const DevKv8& c, const Kv8Query& q, int n_sel, int
     // rows of up to 512 blocks by 256 threads each, so that more of them run at once: 4,096 rows
     // of 256 blocks, with the scores, 104 us with 1,024 threads and 59 with 256, one row of 8 heads
     // over 512 blocks 8.0 and 7.2 (512 rows of 768 blocks 36.4 and 37.7)
+    // A thread's keys stay in registers, as few as the row's blocks need, since every one of them is
+    // looked at whether it is there or not; keys kept in the scores' place have no limit but are read
+    // again.  Scores and selection for 8 rows, us, by keys a thread (0: in place): 2,048 blocks 2: 7.9,
+    // 8: 9.2, 17: 11.3, 0: 9.2; 4,096 blocks 8: 10.5, 17: 12.8, 0: 10.9; 8,192 blocks 8: 11.6, 17: 13.7,
+    // 0: 13.0; 12,000 blocks 17: 14.6, 24: 16.5, 0: 15.1; 17,408 blocks 17: 16.9, 24: 18.4, 0: 19.7; of 128
+    // rows, 17,408 blocks 17: 78.6, 24: 82.4, 0: 96.8.  24,000 blocks 24: 20.5, 0: 24.0.
     const bool small = c.max_blocks <= 512;
     const auto select = small                       ? k_kv8_select<2, 256>
                         : c.max_blocks <= 2 * 1024  ? k_kv8_select<2, 1024>
