@@ -11,6 +11,7 @@ namespace csa2 {
 // Sticky status bits ORed into the workspace status word by kernels.
 constexpr uint32_t kStatusBounds = 1u;
 constexpr uint32_t kStatusTimeout = 2u;
+constexpr uint32_t kStatusNonFinite = 4u;   // input values that were not finite (kv8_cache.cu)
 
 // A by-value copy of csa2_cache plus the derived per-sequence capacity.
 struct DevCache {

@@ -8,9 +8,6 @@
 
 namespace csa2 {
 
-// A status bit beside common.cuh's: input values that were not finite (kv8_cache.cu).
-constexpr uint32_t kStatusNonFinite = 4u;
-
 // Tries of the bounded mbarrier waits that guard work (not the drains that
 // wait for copies and MMAs already in flight) in the kernels launched from now
 // on; csa2_debug_set_wait_limit sets it (a diagnostic: 0 makes those waits
