@@ -36,7 +36,8 @@
 // Work split as in kv8_attn.cu: the (row block, head, 128 positions) steps of
 // the batch, and kItem units an item, form one line cut into equal pieces; cut
 // items are merged by k_kv8_prefill_combine.  2,048 tokens over 8,192 positions
-// (32 / 8 heads of 128): 270 us = 0.89 PFLOP/s, 53 % of the measured bf16 rate.  A
+// (32 / 8 heads of 128): 268 to 282 us on different boards, 285 called from Python
+// = 0.84 PFLOP/s, half the measured bf16 rate.  A
 // step of a row tile is a chain of about 4,100 cycles (S to registers 250, weights
 // 1,500, the halves' agreement and the store 500, both products 1,100, looks at
 // barriers the rest), of which the other tile's covers a half.

@@ -558,7 +558,10 @@ typedef struct {
 
 /*
  * Bytes of workspace for the kv8 calls with T query rows of H heads and, where
- * blocks are selected, n_sel of them (0: none).  0 on invalid arguments.
+ * blocks are selected, n_sel of them (0: none): some 3 to 40 MB for partial
+ * results, and for a selection the scores, batch * T * n_kv_heads * max_blocks
+ * floats (2,048 tokens over 16,384 blocks of 8 heads: 1 GiB; a caller short of
+ * memory selects for fewer tokens a call).  0 on invalid arguments.
  * Cleared once with csa2_workspace_init; calls on one stream may share it.
  */
 CSA2_API size_t csa2_kv8_workspace_bytes(const csa2_kv8_cache* cache, int T, int H, int n_sel);
@@ -610,8 +613,9 @@ CSA2_API csa2_status csa2_kv8_read(const csa2_kv8_cache* cache, const int32_t* s
  *     lse = log sum_t exp(z_t)      fp32 [batch][T][H], nullable
  * q is CSA2_BF16 or CSA2_F16.  A row that sees nothing (p < 0) gives out = 0,
  * lse = -inf.  The products take q and the codes as they are and accumulate in
- * fp32; the weights exp(z - max) are rounded to fp16 for the second product,
- * sums and lse use them unrounded.  What a block holds behind the sequence's
+ * fp32; the weights times the value scales are rounded to fp16 for the second
+ * product (to 2^-11 of each, and to 2^-33 of the row's greatest), sums and lse use
+ * weights that are not rounded.  What a block holds behind the sequence's
  * end does not enter, whatever it is; a block before the windows of all rows is
  * not looked up, so its table entry may be anything.
  */
@@ -629,7 +633,9 @@ CSA2_API csa2_status csa2_kv8_attn(const csa2_kv8_cache* cache, const void* q, c
  *     2^e s sum_d (min(qi_d, 0) lo_d + max(qi_d, 0) hi_d),
  * qi = round-to-nearest-even(q 2^-e), e the least with max |q| <= 127 * 2^e
  * (-118 <= e; channels that are not finite count as 0): an upper bound of
- * every q . k in the block, up to the rounding of q.  The sums are exact.
+ * every q . k in the block, up to the rounding of q.  The sums are exact, and so
+ * is their product with the powers of two within fp32's normal range (taken from
+ * the left: 2^e sum, then s).
  * Bounds cover what the block holds at the time of the call, rows behind p
  * included.  1 <= n_sel <= 2048, n_first + n_recent <= n_sel, max_blocks <=
  * 2^20.
@@ -644,7 +650,7 @@ CSA2_API csa2_status csa2_kv8_select_blocks(const csa2_kv8_cache* cache, const v
  * block_idx[b][j][h / (H / n_kv_heads)][0..n_sel) alone: strictly ascending
  * visible blocks, then -1 (as csa2_kv8_select_blocks writes them).  An entry
  * that breaks this sets CSA2_ERR_DEVICE_BOUNDS, and the call's results are not
- * to be used.  n_sel >= 1.
+ * to be used; as many entries are looked at as the sequence has blocks.  n_sel >= 1.
  */
 CSA2_API csa2_status csa2_kv8_block_attn(const csa2_kv8_cache* cache, const void* q, csa2_dtype q_dtype,
                                          int64_t stride_b, int64_t stride_t, int T, int H, const int32_t* n_q,
