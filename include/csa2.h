@@ -533,7 +533,7 @@ CSA2_API csa2_status csa2_lse_merge(int R, int batch, int H, int dim, const floa
  * slice of a fused projection needs no copy; both strides are multiples of 8).
  * A padded batch gives n (device int32 [batch], 0 <= n[b] <= T): only rows
  * j < n[b] are read, and what an output holds for the others stays as it was.
- * n == NULL means T rows of every sequence.
+ * n == NULL means T rows of every sequence.  T >= 1 but where 0 is allowed.
  *
  * Query row j of sequence b sits at position p = seq_lens[b] - n[b] + j and
  * sees positions t <= p.  H query heads, a multiple of n_kv_heads: head h reads
@@ -612,8 +612,9 @@ CSA2_API csa2_status csa2_kv8_read(const csa2_kv8_cache* cache, const int32_t* s
  *     out = sum_t softmax(z)_t v_t  [batch][T][H][head_dim] of the query's type
  *     lse = log sum_t exp(z_t)      fp32 [batch][T][H], nullable
  * q is CSA2_BF16 or CSA2_F16.  A row that sees nothing (p < 0) gives out = 0,
- * lse = -inf.  The products take q and the codes as they are and accumulate in
- * fp32; the weights times the value scales are rounded to fp16 for the second
+ * lse = -inf.  The products take q and the codes and accumulate in fp32; a bf16 q is
+ * taken as fp16 times a power of two per row: as it is for channels of 2^-31 of the
+ * row's greatest and more, to 2^-39 of the greatest below; the weights times the value scales are rounded to fp16 for the second
  * product (to 2^-11 of each, and to 2^-33 of the row's greatest), sums and lse use
  * weights that are not rounded.  What a block holds behind the sequence's
  * end does not enter, whatever it is; a block before the windows of all rows is

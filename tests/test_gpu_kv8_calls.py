@@ -4,9 +4,51 @@ import pytest
 import torch
 
 import fp4_sparse_attention_csa2_b200 as csa2
-from test_gpu_kv8 import both_caches, fill, i32, same_cache, workspace
+from test_gpu_kv8 import attend, both_caches, check_attn, fill, i32, same_cache, workspace
 
 pytestmark = pytest.mark.gpu
+
+
+def test_a_new_tensor_of_lengths_or_blocks_is_used():
+    lens = [100, 37]
+    dev, r = both_caches(2, 2, 64, 16, 8)
+    fill(dev, r, lens)
+    attend(dev, r, lens, 1, 8)
+    fewer = [60, 37]
+    dev.seq_lens = dev.seq_lens - i32([40, 0])
+    attend(dev, r, fewer, 1, 8)
+    wide = torch.full((2, 12), -1, dtype=torch.int32, device="cuda")
+    wide[:, :8] = dev.block_table
+    dev.block_table = wide                                        # the old table is freed
+    other = torch.full((2, 8), 1 << 20, dtype=torch.int32, device="cuda")
+    attend(dev, r, fewer, 1, 8)
+    attend(dev, r, fewer, 24, 8)
+    assert int(other[0, 0]) == 1 << 20
+
+
+def test_many_rows_captured_once_and_replayed_as_lengths_change():
+    B, T, H = 3, 40, 8
+    dev, r = both_caches(B, 2, 64, 16, 512)
+    full = [700, 300, 90]
+    fill(dev, r, full)
+    q = torch.randn(B, T, H, 64, generator=torch.Generator().manual_seed(4)).bfloat16().cuda()
+    out, lse, n = torch.zeros_like(q), torch.zeros(B, T, H, device="cuda"), i32([T] * B)
+    ws, side = workspace(dev, T, H), torch.cuda.Stream()
+    with torch.cuda.stream(side):
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=side):
+            csa2.kv8_attn(dev, q, out, ws, lse=lse, n_q=n)
+    for lens, rows in ((full, [40, 40, 40]), ([513, 1, 64], [7, 1, 40]), ([0, 300, 17], [0, 33, 0]), (full, [1, 0, 40])):
+        dev.seq_lens.copy_(i32(lens))
+        n.copy_(i32(rows))
+        out.fill_(5.0), lse.fill_(5.0)
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert csa2.read_device_status(ws) == csa2.OK
+        check_attn(dev, r, q, out, lse, rows, 1 / 8, lambda b, j, h, p: np.arange(p + 1), lens)
+        for b in range(B):
+            assert bool((out[b, rows[b]:] == 5).all()) and bool((lse[b, rows[b]:] == 5).all())
 
 
 def test_append_at_a_negative_start_drops_that_sequences_rows_alone():
