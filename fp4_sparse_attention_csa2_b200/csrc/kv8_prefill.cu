@@ -255,9 +255,9 @@ struct Sum {
     }
     // The maximum M rises by d.
     __device__ __forceinline__ void rise(float d) {
+        if (l < 0x1p-40f) normalise();
         if (d <= kApart || l == 0.0f) {
             l *= ex2(-d);
-            if (l < 0x1p-40f) normalise();
         } else {
             const float k = rintf(d);
             l *= ex2(k - d);
@@ -740,7 +740,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv8_prefill(const __grid_consta
                     M = top;
                 }
             }
-            if (!(fabsf(e0 + sum.x) <= 100.0f)) sum.normalise();
+            // parts to be merged, whose units differ, by their own magnitude
+            if (!whole || !(fabsf(e0 + sum.x) <= 100.0f)) sum.normalise();
             // outputs: O 2^e / l, -136 < e <= 120, in two factors, of which the first stays a normal number
             const float l = sum.l, e = e0 + sum.x, scale = ex2(fminf(e + 100.0f, 0.0f));
             const float f = l == 0.0f ? 0.0f : ex2(fmaxf(e, -100.0f)) / l;

@@ -42,7 +42,7 @@ def kernels(call):
     return " ".join(e.name for e in p.events() if "csa2" in e.name)
 
 
-def check(dev, r, lens, T, H, seed=9):
+def check(dev, r, lens, T, H, seed=9, q_scale=1.0):
     """Every row against the definition in 64 bits.
 
     Bounds as kv8_ref.bounds derives them, with two differences.  The weights'
@@ -53,7 +53,7 @@ def check(dev, r, lens, T, H, seed=9):
     """
     B, D, heads, sm = dev.batch, r.D, r.heads, 1 / math.sqrt(r.D)
     G = H // heads
-    q = torch.randn(B, T, H, D, generator=torch.Generator().manual_seed(seed)).bfloat16().cuda()
+    q = (torch.randn(B, T, H, D, generator=torch.Generator().manual_seed(seed)) * q_scale).bfloat16().cuda()
     out, lse = torch.full_like(q, 5.0), torch.full((B, T, H), 5.0, device="cuda")
     ws = workspace(dev, T, H)
     names = kernels(lambda: csa2.kv8_attn(dev, q, out, ws, lse=lse))
@@ -121,3 +121,16 @@ def test_least_scale_over_many_pieces(T, G, room):
     for mags in ([1e-35], [1e-35, 2.0 ** -7, 0.0], [2.0 ** 70, 2.0 ** -70]):
         dev, r = with_values(1, 128, 64, [9000], mags, room=room)
         check(dev, r, [9000], T, G)
+
+
+@pytest.mark.parametrize("q_scale", [1.0, 16.0])
+@pytest.mark.parametrize("mags", [[1.0, 2.0 ** 72, 2.0 ** 56, 1.0, 2.0 ** -60, 2.0 ** 10],
+                                  [2.0 ** 64, 2.0 ** 64, 1.0, 1.0, 1.0, 2.0 ** -64, 2.0 ** 30],
+                                  [1.0, 1.0, 1.0, 1.0, 2.0 ** -100, 2.0 ** -36, 2.0 ** 28, 2.0 ** 92]])
+@pytest.mark.parametrize("L,T,G,heads", [(9000, 60, 4, 1), (2300, 70, 8, 4), (2300, 20, 4, 8),
+                                         (9000, 1, 8, 1), (2300, 4, 4, 4)])
+def test_parts_and_halves_with_units_of_their_own(L, T, G, heads, mags, q_scale):
+    # the parts of a row, its halves and its even and odd steps are added up whatever units their sums are in;
+    # logits of up to some hundred make one of them count for nothing here and there
+    dev, r = with_values(heads, 128, 64, [L], mags, room=T * G > 16)
+    check(dev, r, [L], T, heads * G, q_scale=q_scale)
